@@ -229,6 +229,115 @@ mi_status mi_affine_scan_bwd_h0(const void *A, const void *Abar, const void *H, 
                                 int64_t B, int64_t T, int64_t n, int64_t k, int64_t v, mi_dtype dt,
                                 void *ws, size_t ws_bytes, hipStream_t stream);
 
+/* ------------------------------------------------------------------------ */
+/* Block operators: what a recurrent sequence layer runs around its scan.   */
+/*                                                                          */
+/* Activations (x, u, delta, z, Bm, Cm and their gradients) have the dtype  */
+/* `dt`; parameters (w, bias, A, skip, delta_bias and their gradients) and  */
+/* scan states are fp32.  All arithmetic is fp32.  Results are bitwise      */
+/* reproducible: sums over rows and channels have a fixed order and no      */
+/* floating-point atomics are used.  `lengths` (B int32 on the device, or   */
+/* NULL for T each) gives every sequence its own length; values are clamped */
+/* to [0, T].  Steps at or past it are not read into any result (they may   */
+/* hold anything, NaN included); outputs and gradients there are zero.      */
+/* ------------------------------------------------------------------------ */
+
+typedef enum {
+    MI_ACT_NONE = 0,
+    MI_ACT_SILU = 1 /* x / (1 + exp(-x)) */
+} mi_act;
+
+/* Causal convolution, depthwise, channels last.  x (B,T,D), w (D,K), bias (D)
+ * or NULL, x0 (B,K-1,D) the inputs before the first step or NULL for zeros.
+ * With xe = [x0 ; x] along time:
+ *     s_t = bias + sum_{k<K} w[:,k] xe_{t+k},   y_t = act(s_t),
+ * and xT (B,K-1,D), or NULL: the K-1 inputs that end at the sequence's
+ * length, the x0 of its continuation (an exact copy).  1 <= K <= 8.
+ * With K = 1, x0 and xT hold nothing and are not used. */
+mi_status mi_causal_conv_fwd(const void *x, const float *w, const float *bias, const void *x0,
+                             const int32_t *lengths, void *y, void *xT, int64_t B, int64_t T,
+                             int64_t D, int64_t K, mi_act act, mi_dtype dt, hipStream_t stream);
+
+/* Gradient of the above for the upstream gradients dy (B,T,D) and dxT
+ * (B,K-1,D) or NULL: dx (B,T,D), dw (D,K), dbias (D) or NULL, dx0 (B,K-1,D) or
+ * NULL.  s is recomputed.  ds = dy act'(s); dx_t = sum_k w[:,k] ds_{t+K-1-k}
+ * (+ dxT); dw[:,k] = sum_{b,t} ds_t xe_{t+k}; dbias = sum ds. */
+size_t mi_causal_conv_bwd_workspace(int64_t B, int64_t T, int64_t D, int64_t K, mi_dtype dt);
+mi_status mi_causal_conv_bwd(const void *x, const float *w, const float *bias, const void *x0,
+                             const int32_t *lengths, const void *dy, const void *dxT, void *dx,
+                             float *dw, float *dbias, void *dx0, int64_t B, int64_t T, int64_t D,
+                             int64_t K, mi_act act, mi_dtype dt, void *ws, size_t ws_bytes,
+                             hipStream_t stream);
+
+/* One step of the convolution: x (B,D), x0 (B,K-1,D) -> y (B,D) and x_out
+ * (B,K-1,D), x0 shifted by one with x appended.  x_out may be x0 itself
+ * (update in place); no other overlap is allowed. */
+mi_status mi_causal_conv_step(const void *x, const float *w, const float *bias, const void *x0,
+                              void *y, void *x_out, int64_t B, int64_t D, int64_t K, mi_act act,
+                              mi_dtype dt, hipStream_t stream);
+
+/* Selective state-space scan: N states a channel, with gates formed from the
+ * token.  u, delta, z (B,T,D); A (D,N); Bm, Cm (B,T,G,N), one row for the D/G
+ * channels of a group; skip, delta_bias (D); h0, hT (B,D,N).  z, skip,
+ * delta_bias, h0, hT may be NULL.  1 <= N <= 64, G divides D.
+ *     dl_t = softplus(delta_t + delta_bias)       (softplus = 0: delta + bias)
+ *     h_t[n] = exp(dl_t A[n]) h_{t-1}[n] + dl_t u_t Bm_t[n],   h_0 = h0
+ *     s_t = sum_n Cm_t[n] h_t[n] + skip u_t,   y_t = s_t silu(z_t)
+ * hT is the state at the sequence's length.  `states`, or NULL, receives what
+ * the backward needs: the fp32 state before every block of
+ * mi_selective_scan_block(N) steps, (B, ceil(T/block), D, N). */
+int64_t mi_selective_scan_block(int64_t N);
+mi_status mi_selective_scan_fwd(const void *u, const void *delta, const float *A, const void *Bm,
+                                const void *Cm, const float *skip, const void *z,
+                                const float *delta_bias, const float *h0, const int32_t *lengths,
+                                void *y, float *hT, float *states, int64_t B, int64_t T, int64_t D,
+                                int64_t G, int64_t N, int softplus, mi_dtype dt,
+                                hipStream_t stream);
+
+/* Gradient for the upstream gradients dy (B,T,D) and dhT (B,D,N) or NULL.
+ * `states` is the forward's.  dskip, dz, ddelta_bias go with skip, z and
+ * delta_bias (NULL together); dh0 may be NULL.  With ds = dy silu(z),
+ * g_t = Cm_t ds_t + a_{t+1} g_{t+1} (g_T includes dhT), q_t = g_t a_t h_{t-1}:
+ *     dCm_t = sum_ch ds_t h_t,  dBm_t = sum_ch g_t dl_t u_t,
+ *     dA = sum_t q_t dl_t,      ddl_t = sum_n q_t A + u_t sum_n g_t Bm_t,
+ *     du_t = dl_t sum_n g_t Bm_t + skip ds_t,   dh0 = a_1 g_1. */
+size_t mi_selective_scan_bwd_workspace(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N, mi_dtype dt);
+mi_status mi_selective_scan_bwd(const void *u, const void *delta, const float *A, const void *Bm,
+                                const void *Cm, const float *skip, const void *z,
+                                const float *delta_bias, const float *states,
+                                const int32_t *lengths, const void *dy, const float *dhT, void *du,
+                                void *ddelta, float *dA, void *dBm, void *dCm, float *dskip,
+                                void *dz, float *ddelta_bias, float *dh0, int64_t B, int64_t T,
+                                int64_t D, int64_t G, int64_t N, int softplus, mi_dtype dt,
+                                void *ws, size_t ws_bytes, hipStream_t stream);
+
+/* One step of the scan: u, delta, z (B,D), Bm, Cm (B,G,N), h (B,D,N) -> y (B,D)
+ * and h_out (B,D,N), which may be h itself (update in place). */
+mi_status mi_selective_scan_step(const void *u, const void *delta, const float *A, const void *Bm,
+                                 const void *Cm, const float *h, const float *skip, const void *z,
+                                 const float *delta_bias, void *y, float *h_out, int64_t B,
+                                 int64_t D, int64_t G, int64_t N, int softplus, mi_dtype dt,
+                                 hipStream_t stream);
+
+/* Group norm, channels last: x (R,D), the D/G channels of a group of one row
+ * are normalised together (nothing crosses rows, so it is causal in time).
+ *     xh = (x - mean) / sqrt(var + eps)             (centered)
+ *     xh = x / sqrt(mean(x^2) + eps)                (not centered)
+ *     p = xh w + bias,   y = act(p) silu(z)
+ * w, bias (D) and z (R,D) may be NULL; act and z exclude each other. */
+mi_status mi_group_norm_fwd(const void *x, const float *w, const float *bias, const void *z,
+                            void *y, int64_t R, int64_t D, int64_t G, float eps, int centered,
+                            mi_act act, mi_dtype dt, hipStream_t stream);
+
+/* Gradient for the upstream gradient dy (R,D): dx (R,D), dw, dbias (D), dz (R,D);
+ * dw, dbias and dz go with w, bias and z (NULL together).  The statistics are
+ * recomputed from x. */
+size_t mi_group_norm_bwd_workspace(int64_t R, int64_t D, int64_t G, mi_dtype dt);
+mi_status mi_group_norm_bwd(const void *x, const float *w, const float *bias, const void *z,
+                            const void *dy, void *dx, float *dw, float *dbias, void *dz, int64_t R,
+                            int64_t D, int64_t G, float eps, int centered, mi_act act, mi_dtype dt,
+                            void *ws, size_t ws_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

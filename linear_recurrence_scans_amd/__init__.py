@@ -44,7 +44,7 @@ _DTYPES = {torch.float32: MI_F32, torch.bfloat16: MI_BF16, torch.float16: MI_F16
 
 # C ABI entry points and their argument types.
 _V, _I64, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t
-_I = ctypes.c_int
+_I, _F = ctypes.c_int, ctypes.c_float
 _SIGS = {
     "mi_status_string": ([_I], ctypes.c_char_p),
     "mi_device_check": ([_I, ctypes.c_char_p, _SZ], _I),
@@ -62,6 +62,18 @@ _SIGS = {
     "mi_affine_scan_bwd": ([_V] * 7 + [_I64] * 5 + [_I, _V, _SZ, _V], _I),
     "mi_affine_scan_fwd_h0": ([_V] * 5 + [_I64] * 5 + [_I, _V, _SZ, _V], _I),
     "mi_affine_scan_bwd_h0": ([_V] * 9 + [_I64] * 5 + [_I, _V, _SZ, _V], _I),
+    "mi_causal_conv_fwd": ([_V] * 7 + [_I64] * 4 + [_I, _I, _V], _I),
+    "mi_causal_conv_bwd_workspace": ([_I64] * 4 + [_I], _SZ),
+    "mi_causal_conv_bwd": ([_V] * 11 + [_I64] * 4 + [_I, _I, _V, _SZ, _V], _I),
+    "mi_causal_conv_step": ([_V] * 6 + [_I64] * 3 + [_I, _I, _V], _I),
+    "mi_selective_scan_block": ([_I64], _I64),
+    "mi_selective_scan_fwd": ([_V] * 13 + [_I64] * 5 + [_I, _I, _V], _I),
+    "mi_selective_scan_bwd_workspace": ([_I64] * 5 + [_I], _SZ),
+    "mi_selective_scan_bwd": ([_V] * 21 + [_I64] * 5 + [_I, _I, _V, _SZ, _V], _I),
+    "mi_selective_scan_step": ([_V] * 11 + [_I64] * 4 + [_I, _I, _V], _I),
+    "mi_group_norm_fwd": ([_V] * 5 + [_I64] * 3 + [_F, _I, _I, _I, _V], _I),
+    "mi_group_norm_bwd_workspace": ([_I64] * 3 + [_I], _SZ),
+    "mi_group_norm_bwd": ([_V] * 9 + [_I64] * 3 + [_F, _I, _I, _I, _V, _SZ, _V], _I),
 }
 
 _lib = None
@@ -539,3 +551,10 @@ def affine_scan_fwd(A, Bm):
 
 def affine_scan_bwd(A, Abar, Bbar, gAbar, gBbar):
     return mi_affine_scan_bwd(A, Abar, Bbar, gAbar, gBbar)
+
+
+# The block operators live in a module of their own and share the helpers above.
+from . import block_ops as _block_ops  # noqa: E402
+from .block_ops import *  # noqa: E402,F401,F403
+
+__all__ += _block_ops.__all__

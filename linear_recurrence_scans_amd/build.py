@@ -17,7 +17,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmiscan.so")
-SOURCES = ["api.hip", "linear_scan.hip", "log_scan.hip", "affine_scan.hip"]
+SOURCES = ["api.hip", "linear_scan.hip", "log_scan.hip", "affine_scan.hip",
+           "causal_conv.hip", "selective_scan.hip", "selective_scan_bwd.hip", "group_norm.hip"]
 # The benchmark's probe kernels (streaming ceiling, cache flush): a library of
 # their own, not part of libmiscan.so.
 BENCH_LIB = os.path.join(PKG, "libmiscan_bench.so")

@@ -1,0 +1,89 @@
+// block_ops.hpp -- device helpers shared by the block operators (causal
+// convolution, selective scan, group norm): one-element IO, the activations
+// and the fixed-order sum over partial results.
+#pragma once
+
+#include "common.hpp"
+
+namespace miscan {
+
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float LN2 = 0.6931471805599453f;
+
+template <typename T>
+__device__ __forceinline__ float ld1(const T *p) {
+    float f;
+    Pack<T, 1>::unpack(*reinterpret_cast<const typename Pack<T, 1>::raw_t *>(p), &f);
+    return f;
+}
+template <typename T>
+__device__ __forceinline__ void st1(T *p, float f) {
+    *reinterpret_cast<typename Pack<T, 1>::raw_t *>(p) = Pack<T, 1>::pack(&f);
+}
+
+// exp(x) as exp2 of the rounded product: its relative error grows as |x| 2^-24,
+// which the factors it is used in (x sigmoid(x), decays) damp again.
+__device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * LOG2E); }
+__device__ __forceinline__ float sigmoid(float x) { return __builtin_amdgcn_rcpf(1.f + fast_exp(-x)); }
+__device__ __forceinline__ float silu(float x) { return x * sigmoid(x); }
+// d silu / dx from x and g = sigmoid(x)
+__device__ __forceinline__ float dsilu(float x, float g) { return g * fmaf(x, 1.f - g, 1.f); }
+
+// softplus(x) = max(x, 0) + log1p(e), e = exp(-|x|), with a relative error of a
+// few 2^-24 where the result is small too (x far below zero): log1p by its
+// series for e < 1/16, else log2(1 + e) plus the rounding error of 1 + e.
+// *sig receives sigmoid(x), the derivative.
+__device__ __forceinline__ float softplus(float x, float *sig) {
+    const float e = fast_exp(-fabsf(x));
+    const float u = 1.f + e;
+    const float r = __builtin_amdgcn_rcpf(u);
+    const float big = fmaf(__builtin_amdgcn_logf(u), LN2, (e - (u - 1.f)) * r);
+    float p = fmaf(e, -1.f / 6.f, 1.f / 5.f);
+    p = fmaf(e, p, -1.f / 4.f);
+    p = fmaf(e, p, 1.f / 3.f);
+    p = fmaf(e, p, -1.f / 2.f);
+    p = fmaf(e, p, 1.f);
+    const float l = e < 0.0625f ? e * p : big;
+    *sig = x >= 0.f ? r : e * r;
+    return fmaxf(x, 0.f) + l;
+}
+
+// The length of sequence b: lengths[b] clamped to [0, T], or T.
+__device__ __forceinline__ int64_t seq_len(const int32_t *lengths, int64_t b, int64_t T) {
+    if (lengths == nullptr) return T;
+    const int64_t n = lengths[b];
+    return n < 0 ? 0 : n > T ? T : n;
+}
+
+// Sum of P partial rows of M floats, handed to st(m, sum): 64 columns a
+// workgroup, four threads a column that each add every fourth row, joined in a
+// fixed order.  Reads each partial once with 256-byte rows.
+template <class Store>
+__global__ __launch_bounds__(256) void reduce_parts_kernel(const float *part, int64_t P, int64_t M, Store st) {
+    __shared__ float acc[4][64];
+    const int col = threadIdx.x & 63, row = threadIdx.x >> 6;
+    for (int64_t m0 = (int64_t)blockIdx.x * 64; m0 < M; m0 += (int64_t)gridDim.x * 64) {
+        const int64_t m = m0 + col;
+        float s = 0.f;
+        if (m < M) {
+            const float *q = part + m;
+#pragma unroll 4
+            for (int64_t p = row; p < P; p += 4) s += q[p * M];
+        }
+        acc[row][col] = s;
+        __syncthreads();
+        if (row == 0 && m < M) st(m, (acc[0][col] + acc[1][col]) + (acc[2][col] + acc[3][col]));
+        __syncthreads();
+    }
+}
+
+template <class Store>
+inline mi_status reduce_parts(const float *part, int64_t P, int64_t M, Store st, hipStream_t s) {
+    if (M == 0) return MI_OK;
+    const int64_t blocks = (M + 63) / 64;
+    hipLaunchKernelGGL(reduce_parts_kernel<Store>, dim3((unsigned)(blocks < 16384 ? blocks : 16384)), dim3(256), 0,
+                       s, part, P, M, st);
+    return launch_status();
+}
+
+}  // namespace miscan

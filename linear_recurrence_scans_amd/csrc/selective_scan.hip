@@ -1,0 +1,352 @@
+// selective_scan.hip -- the selective state-space scan: forward and the
+// single-token step (the gradient is in selective_scan_bwd.hip).
+//
+// Per channel, state and step: the gate's exponent (mul), the gate (exp2), the
+// input dl u Bm (mul), the state (fma), the output (fma), and for the carry a
+// running product of gates applied to the state that entered the wave (mul) and
+// its output (fma).  An exp2 takes two issue slots, so a state-step costs at
+// least 8 slots of the vector ALU; with N = 16 states that is above the time of
+// the 6 to 8 bytes a channel-step moves: the vector ALU is the bound.
+#include "checks.hpp"
+#include "selective_scan.hpp"
+
+namespace miscan {
+namespace {
+
+template <typename T, int S, int C, int L, int NW>
+__global__ __launch_bounds__(NW * 64) void scan_fwd_kernel(ScanArgs p) {
+    constexpr int EL = S * C, J = L / 4, NP = 4 * S;
+    constexpr int E = EL * 64;                      // states a tile
+    constexpr int NT = NW * 64;
+    constexpr int FPT = (E + NT - 1) / NT;          // folded states a thread
+    constexpr int BPL = (L * NP + 63) / 64;         // Bm (Cm) values a lane loads
+    using LV = LaneVec<EL>;
+    __shared__ __align__(16) float sm_x[NW][L][16][2 * C];  // dl, dl u
+    __shared__ __align__(16) float sm_b[NW][2][L][NP];      // Bm, Cm
+    __shared__ __align__(16) float sm_s[NW][E], sm_p[NW][E];
+    const int item = xcd_item(p.n_items);
+    if (item >= p.n_items) return;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int sg = lane >> 4, cl = lane & 15;
+    const int tile = item % p.tiles;
+    const int g = item / p.tiles % p.G;
+    const int64_t b = item / p.tiles / p.G;
+    const int ch0 = tile * 16 * C;                  // first channel of the tile inside its group
+    const int64_t d0 = (int64_t)g * p.per + ch0;
+    const int nch = p.per - ch0 < 16 * C ? p.per - ch0 : 16 * C;
+    const int nv = nch - cl * C < 0 ? 0 : nch - cl * C > C ? C : nch - cl * C;
+    const int64_t dl0 = d0 + cl * C;                // this lane's first channel
+    const int64_t len = seq_len(p.lengths, b, p.T);
+    const bool vec = p.vec;
+    float A2[S][C], skip[C], bias[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const bool ok = c < nv;
+        skip[c] = ok && p.skip ? p.skip[dl0 + c] : 0.f;
+        bias[c] = ok && p.delta_bias ? p.delta_bias[dl0 + c] : 0.f;
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            const int n = sg * S + s;
+            A2[s][c] = ok && n < p.N ? p.A[(dl0 + c) * p.N + n] * LOG2E : 0.f;
+        }
+    }
+    // folded states: thread tid carries positions tid, tid + NT, ... of the tile
+    float carry[FPT];
+    int64_t st_off[FPT];  // offset in (D, N), or -1
+#pragma unroll
+    for (int f = 0; f < FPT; ++f) {
+        const int i = tid + f * NT;
+        int ln, e;
+        LV::where(i < E ? i : 0, &ln, &e);
+        const int n = (ln >> 4) * S + e % S, ch = (ln & 15) * C + e / S;
+        st_off[f] = i < E && n < p.N && ch < nch ? (d0 + ch) * p.N + n : -1;
+        carry[f] = st_off[f] >= 0 && p.h0 ? p.h0[b * p.D * p.N + st_off[f]] : 0.f;
+    }
+    const T *u = static_cast<const T *>(p.u) + b * p.T * p.D + dl0;
+    const T *delta = static_cast<const T *>(p.delta) + b * p.T * p.D + dl0;
+    const T *z = p.z ? static_cast<const T *>(p.z) + b * p.T * p.D + dl0 : nullptr;
+    const T *Bm = static_cast<const T *>(p.Bm) + (b * p.T * p.G + g) * p.N;
+    const T *Cm = static_cast<const T *>(p.Cm) + (b * p.T * p.G + g) * p.N;
+    T *y = static_cast<T *>(p.y) + b * p.T * p.D + dl0;
+    const int64_t brow = (int64_t)p.G * p.N;
+    const int64_t n_state_blocks = p.states ? (p.T + scan_block_of<S>() - 1) / scan_block_of<S>() : 0;
+
+    for (int64_t tb = 0; tb < p.T; tb += NW * L) {
+        const int64_t t0 = tb + wave * L;
+        // this wave's rows: dl and dl u by the lanes that own them
+        float uu[J][C], zz[J][C];
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int64_t t = t0 + 4 * j + sg;
+            const int n_ok = t < len ? nv : 0;
+            float dd[C];
+            load_ch<T, C>(u + t * p.D, n_ok, vec, uu[j]);
+            load_ch<T, C>(delta + t * p.D, n_ok, vec, dd);
+            if (z) load_ch<T, C>(z + t * p.D, n_ok, vec, zz[j]);
+            float o[2 * C];
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                float unused;
+                const float r = gate_rate(dd[c] + bias[c], p.softplus, &unused);
+                o[c] = c < n_ok ? r : 0.f;
+                o[C + c] = o[c] * uu[j][c];
+            }
+#pragma unroll
+            for (int i = 0; i < 2 * C; ++i) sm_x[wave][4 * j + sg][cl][i] = o[i];
+        }
+#pragma unroll
+        for (int i = 0; i < BPL; ++i) {
+            const int q = lane + 64 * i, t = q / NP, n = q % NP;
+            const bool ok = q < L * NP && t0 + t < len && n < p.N;
+            const float bv = ok ? ld1(Bm + (t0 + t) * brow + n) : 0.f;
+            const float cv = ok ? ld1(Cm + (t0 + t) * brow + n) : 0.f;
+            if (q < L * NP) {
+                sm_b[wave][0][t][n] = bv;
+                sm_b[wave][1][t][n] = cv;
+            }
+        }
+        wave_lds_fence();
+        // the wave's steps from a zero state
+        float a[L][S][C], h[S][C], yl[L][C], sum[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            sum[c] = 0.f;
+#pragma unroll
+            for (int s = 0; s < S; ++s) h[s][c] = 0.f;
+        }
+#pragma unroll
+        for (int t = 0; t < L; ++t) {
+            float dx[2 * C], bt[S], ct[S];
+            __builtin_amdgcn_sched_barrier(0);
+            lds_read<2 * C>(sm_x[wave][t][cl], dx);
+            lds_read<S>(&sm_b[wave][0][t][sg * S], bt);
+            lds_read<S>(&sm_b[wave][1][t][sg * S], ct);
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                sum[c] += dx[c];
+                yl[t][c] = 0.f;
+#pragma unroll
+                for (int s = 0; s < S; ++s) {
+                    a[t][s][c] = __builtin_amdgcn_exp2f(dx[c] * A2[s][c]);
+                    h[s][c] = fmaf(a[t][s][c], h[s][c], dx[C + c] * bt[s]);
+                    yl[t][c] = fmaf(ct[s], h[s][c], yl[t][c]);
+                }
+            }
+        }
+        float hv[EL], pv[EL];
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                hv[c * S + s] = h[s][c];
+                pv[c * S + s] = __builtin_amdgcn_exp2f(sum[c] * A2[s][c]);
+            }
+        LV::write(sm_s[wave], lane, hv);
+        LV::write(sm_p[wave], lane, pv);
+        __syncthreads();
+#pragma unroll
+        for (int f = 0; f < FPT; ++f) {
+            const int i = tid + f * NT;
+            if (i < E) {
+                float c = carry[f];
+#pragma unroll
+                for (int w = 0; w < NW; ++w) {
+                    if (p.states && st_off[f] >= 0 && tb + w * L < p.T && (tb + w * L) % scan_block_of<S>() == 0)
+                        p.states[(b * n_state_blocks + (tb + w * L) / scan_block_of<S>()) * p.D * p.N + st_off[f]] = c;
+                    const float s = sm_s[w][i];
+                    sm_s[w][i] = c;
+                    c = fmaf(sm_p[w][i], c, s);
+                }
+                carry[f] = c;
+            }
+        }
+        __syncthreads();
+        // the state that entered the wave, carried through its gates
+        LV::read(sm_s[wave], lane, hv);
+#pragma unroll
+        for (int t = 0; t < L; ++t) {
+            float ct[S];
+            __builtin_amdgcn_sched_barrier(0);
+            lds_read<S>(&sm_b[wave][1][t][sg * S], ct);
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int s = 0; s < S; ++s) {
+                    hv[c * S + s] *= a[t][s][c];
+                    yl[t][c] = fmaf(ct[s], hv[c * S + s], yl[t][c]);
+                }
+        }
+        float out[J][C];
+        sg_join<L, C>(yl, out);
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int64_t t = t0 + 4 * j + sg;
+            if (t < p.T) {
+                float o[C];
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    o[c] = fmaf(skip[c], uu[j][c], out[j][c]);
+                    if (z) o[c] *= silu(zz[j][c]);
+                    if (t >= len) o[c] = 0.f;
+                }
+                store_ch<T, C>(y + t * p.D, nv, vec, o);
+            }
+        }
+    }
+    if (p.hT)
+#pragma unroll
+        for (int f = 0; f < FPT; ++f)
+            if (st_off[f] >= 0) p.hT[b * p.D * p.N + st_off[f]] = carry[f];
+}
+
+// One token: a lane owns up to four states of a channel, LQ lanes a channel.
+// The state is read and written once, which is nearly all the traffic.
+template <typename T>
+__global__ __launch_bounds__(256) void scan_step_kernel(ScanArgs p, int lq, int64_t n_ch) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t chan = i / lq;  // b * D + d
+    const int q = (int)(i % lq);
+    const bool live = chan < n_ch;
+    float acc = 0.f;
+    int64_t b = 0, d = 0;
+    if (live) {
+        b = chan / p.D;
+        d = chan - b * p.D;
+        const float uu = ld1(static_cast<const T *>(p.u) + chan);
+        const float raw = ld1(static_cast<const T *>(p.delta) + chan) + (p.delta_bias ? p.delta_bias[d] : 0.f);
+        float unused;
+        const float dl = gate_rate(raw, p.softplus, &unused);
+        const float x = dl * uu;
+        const int64_t brow = (b * p.G + d / p.per) * p.N;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            const int64_t n = q * 4 + s;
+            if (n < p.N) {
+                const float a = __builtin_amdgcn_exp2f(dl * (p.A[d * p.N + n] * LOG2E));
+                const float h = fmaf(a, p.h0[chan * p.N + n], x * ld1(static_cast<const T *>(p.Bm) + brow + n));
+                p.hT[chan * p.N + n] = h;
+                acc = fmaf(ld1(static_cast<const T *>(p.Cm) + brow + n), h, acc);
+            }
+        }
+        if (q == 0 && p.skip) acc = fmaf(p.skip[d], uu, acc);
+    }
+    for (int m = 1; m < lq; m *= 2) acc += __shfl_xor(acc, m);
+    if (live && q == 0) {
+        if (p.z) acc *= silu(ld1(static_cast<const T *>(p.z) + chan));
+        st1(static_cast<T *>(p.y) + chan, acc);
+    }
+}
+
+template <typename T, int S>
+mi_status launch_fwd(ScanArgs a, hipStream_t s) {
+    using TL = ScanTile<S>;
+    a.tiles = (a.per + 16 * TL::C - 1) / (16 * TL::C);
+    int64_t items;
+    if (!mul_ok(a.B, a.G, a.tiles, 1, &items) || items > 0x7ffffff0) return MI_ERR_UNSUPPORTED;
+    a.n_items = (int)items;
+    hipLaunchKernelGGL((scan_fwd_kernel<T, S, TL::C, TL::L, SCAN_NW>), dim3(xcd_grid(a.n_items)), dim3(SCAN_NW * 64),
+                       0, s, a);
+    return launch_status();
+}
+template <typename T>
+mi_status launch_fwd_t(const ScanArgs &a, hipStream_t s) {
+    switch (scan_s(a.N)) {
+        case 1: return launch_fwd<T, 1>(a, s);
+        case 2: return launch_fwd<T, 2>(a, s);
+        case 4: return launch_fwd<T, 4>(a, s);
+        case 8: return launch_fwd<T, 8>(a, s);
+    }
+    return launch_fwd<T, 16>(a, s);
+}
+
+}  // namespace
+
+mi_status check_scan(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N, mi_dtype dt, ScanSizes *s) {
+    if (B < 0 || T < 0 || D < 0 || G < 1 || N < 0) return MI_ERR_INVALID_ARG;
+    if (!dtype_known(dt) || N < 1 || N > 64) return MI_ERR_UNSUPPORTED;
+    if (D % G != 0) return MI_ERR_INVALID_ARG;
+    const int64_t es = (int64_t)elem_size(dt);
+    int64_t gn;
+    if (!mul_ok(B, T, D, es, &s->x) || !mul_ok(G, N, es, 1, &gn) || !mul_ok(B, T, gn, 1, &s->bc) ||
+        !mul_ok(B, D, N, 4, &s->h) || !mul_ok(D, N, 4, 1, &s->a))
+        return MI_ERR_INVALID_ARG;
+    s->d = D * 4;
+    const int64_t blk = scan_block(N);
+    if (!mul_ok(s->h, T / blk + (T % blk != 0), 1, 1, &s->states)) return MI_ERR_INVALID_ARG;
+    return MI_OK;
+}
+
+// Rows may be read C channels at a time: groups of even width, even row starts,
+// pointers aligned to the pair.
+bool scan_vec(const ScanArgs &a, mi_dtype dt) {
+    const Buf b[8] = {{a.u, 1}, {a.delta, 1}, {a.z, 1}, {a.y, 1}, {a.dy, 1}, {a.du, 1}, {a.ddelta, 1}, {a.dz, 1}};
+    return a.D % 2 == 0 && a.per % 2 == 0 && pick_vec(2, elem_size(dt), b, 8) == 2;
+}
+
+}  // namespace miscan
+
+using namespace miscan;
+
+extern "C" {
+
+int64_t mi_selective_scan_block(int64_t N) { return N < 1 || N > 64 ? 0 : scan_block(N); }
+
+mi_status mi_selective_scan_fwd(const void *u, const void *delta, const float *A, const void *Bm, const void *Cm,
+                                const float *skip, const void *z, const float *delta_bias, const float *h0,
+                                const int32_t *lengths, void *y, float *hT, float *states, int64_t B, int64_t T,
+                                int64_t D, int64_t G, int64_t N, int softplus_on, mi_dtype dt, hipStream_t stream) {
+    ScanSizes s;
+    mi_status st = check_scan(B, T, D, G, N, dt, &s);
+    if (st != MI_OK) return st;
+    if (B == 0 || D == 0 || (T == 0 && hT == nullptr)) return MI_OK;
+    const size_t es = elem_size(dt);
+    BufList in, out;
+    in.need(u, s.x, es).need(delta, s.x, es).need(A, s.a, 4).need(Bm, s.bc, es).need(Cm, s.bc, es);
+    in.opt(skip, s.d, 4).opt(z, s.x, es).opt(delta_bias, s.d, 4).opt(h0, s.h, 4).opt(lengths, B * 4, 4);
+    out.need(y, s.x, es).opt(hT, s.h, 4).opt(states, s.states, 4);
+    if ((st = check_lists(in, out)) != MI_OK) return st;
+    ScanArgs a{};
+    a.u = u; a.delta = delta; a.z = z; a.Bm = Bm; a.Cm = Cm; a.A = A; a.skip = skip; a.delta_bias = delta_bias;
+    a.h0 = h0; a.lengths = lengths; a.y = y; a.hT = hT; a.states = states;
+    a.B = B; a.T = T; a.D = D; a.N = N; a.softplus = softplus_on != 0;
+    if (D / G > 0x40000000 || G > 0x40000000) return MI_ERR_UNSUPPORTED;
+    a.G = (int)G; a.per = (int)(D / G);
+    a.vec = scan_vec(a, dt);
+    if (dt == MI_F32) return launch_fwd_t<float>(a, stream);
+    if (dt == MI_BF16) return launch_fwd_t<bf16_t>(a, stream);
+    return launch_fwd_t<f16_t>(a, stream);
+}
+
+mi_status mi_selective_scan_step(const void *u, const void *delta, const float *A, const void *Bm, const void *Cm,
+                                 const float *h, const float *skip, const void *z, const float *delta_bias, void *y,
+                                 float *h_out, int64_t B, int64_t D, int64_t G, int64_t N, int softplus_on,
+                                 mi_dtype dt, hipStream_t stream) {
+    ScanSizes s;
+    mi_status st = check_scan(B, 1, D, G, N, dt, &s);
+    if (st != MI_OK || B == 0 || D == 0) return st;
+    const size_t es = elem_size(dt);
+    BufList in, out;
+    in.need(u, s.x, es).need(delta, s.x, es).need(A, s.a, 4).need(Bm, s.bc, es).need(Cm, s.bc, es);
+    in.opt(skip, s.d, 4).opt(z, s.x, es).opt(delta_bias, s.d, 4);
+    if (h != h_out) in.need(h, s.h, 4);  // in place: the state is checked as an output
+    out.need(y, s.x, es).need(h_out, s.h, 4);
+    if ((st = check_lists(in, out)) != MI_OK) return st;
+    ScanArgs a{};
+    a.u = u; a.delta = delta; a.z = z; a.Bm = Bm; a.Cm = Cm; a.A = A; a.skip = skip; a.delta_bias = delta_bias;
+    a.h0 = h; a.y = y; a.hT = h_out;
+    a.B = B; a.T = 1; a.D = D; a.N = N; a.softplus = softplus_on != 0;
+    if (D / G > 0x40000000 || G > 0x40000000) return MI_ERR_UNSUPPORTED;
+    a.G = (int)G; a.per = (int)(D / G);
+    int lq = 1;
+    while (lq * 4 < N) lq *= 2;
+    const int64_t grid = (B * D * lq + 255) / 256;
+    if (grid > 0x7fffffff) return MI_ERR_UNSUPPORTED;
+    const dim3 gd((unsigned)grid), bd(256);
+    if (dt == MI_F32) hipLaunchKernelGGL(scan_step_kernel<float>, gd, bd, 0, stream, a, lq, B * D);
+    else if (dt == MI_BF16) hipLaunchKernelGGL(scan_step_kernel<bf16_t>, gd, bd, 0, stream, a, lq, B * D);
+    else hipLaunchKernelGGL(scan_step_kernel<f16_t>, gd, bd, 0, stream, a, lq, B * D);
+    return launch_status();
+}
+
+}  // extern "C"
