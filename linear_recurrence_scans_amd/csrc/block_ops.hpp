@@ -29,22 +29,19 @@ __device__ __forceinline__ float silu(float x) { return x * sigmoid(x); }
 // d silu / dx from x and g = sigmoid(x)
 __device__ __forceinline__ float dsilu(float x, float g) { return g * fmaf(x, 1.f - g, 1.f); }
 
-// softplus(x) = max(x, 0) + log1p(e), e = exp(-|x|), with a relative error of a
-// few 2^-24 where the result is small too (x far below zero): log1p by its
-// series for e < 1/16, else log2(1 + e) plus the rounding error of 1 + e.
-// *sig receives sigmoid(x), the derivative.
+// softplus(x) = max(x, 0) + log1p(e), e = exp(-|x|), with a relative error of
+// 3 x 2^-24 where the result is small too (x far below zero): log2 of u = 1 + e
+// is good to 2 x 2^-24 next to 1 as well, and the rounding of u, e - (u - 1), is
+// added times 1 / u, for which 1 - e / 2 is near enough (it is a term of at most
+// 2^-24).  *sig receives sigmoid(x), the derivative, where it is wanted.
 __device__ __forceinline__ float softplus(float x, float *sig) {
     const float e = fast_exp(-fabsf(x));
     const float u = 1.f + e;
-    const float r = __builtin_amdgcn_rcpf(u);
-    const float big = fmaf(__builtin_amdgcn_logf(u), LN2, (e - (u - 1.f)) * r);
-    float p = fmaf(e, -1.f / 6.f, 1.f / 5.f);
-    p = fmaf(e, p, -1.f / 4.f);
-    p = fmaf(e, p, 1.f / 3.f);
-    p = fmaf(e, p, -1.f / 2.f);
-    p = fmaf(e, p, 1.f);
-    const float l = e < 0.0625f ? e * p : big;
-    *sig = x >= 0.f ? r : e * r;
+    const float l = fmaf(__builtin_amdgcn_logf(u), LN2, (e - (u - 1.f)) * fmaf(e, -0.5f, 1.f));
+    if (sig != nullptr) {
+        const float r = __builtin_amdgcn_rcpf(u);
+        *sig = x >= 0.f ? r : e * r;
+    }
     return fmaxf(x, 0.f) + l;
 }
 

@@ -13,16 +13,23 @@
 namespace miscan {
 namespace {
 
-template <typename T, int S, int C, int L, int NW>
-__global__ __launch_bounds__(NW * 64) void scan_fwd_kernel(ScanArgs p) {
+template <typename T, int S, int C, int L, int NW, int WPS>
+__global__ __launch_bounds__(NW * 64, WPS) void scan_fwd_kernel(ScanArgs p) {
     constexpr int EL = S * C, J = L / 4, NP = 4 * S;
     constexpr int E = EL * 64;                      // states a tile
     constexpr int NT = NW * 64;
     constexpr int FPT = (E + NT - 1) / NT;          // folded states a thread
     constexpr int BPL = (L * NP + 63) / 64;         // Bm (Cm) values a lane loads
+    constexpr int LB = L + 4;                       // row stride of Bm in LDS
     using LV = LaneVec<EL>;
-    __shared__ __align__(16) float sm_x[NW][L][16][2 * C];  // dl, dl u
-    __shared__ __align__(16) float sm_b[NW][2][L][NP];      // Bm, Cm
+    using QR = QuadRow<S>;
+    constexpr int NB = QR::NB;
+    using PC = Pack<T, C>;
+    using raw_t = typename PC::raw_t;
+    using one_t = typename Pack<T, 1>::raw_t;
+    __shared__ __align__(16) float sm_x[NW][L][16][2 * C];   // dl, dl u
+    __shared__ __align__(16) float sm_b[NW][NP][LB];         // Bm by state
+    __shared__ __align__(16) float sm_c[NW][L][NP];          // Cm by step
     __shared__ __align__(16) float sm_s[NW][E], sm_p[NW][E];
     const int item = xcd_item(p.n_items);
     if (item >= p.n_items) return;
@@ -36,61 +43,87 @@ __global__ __launch_bounds__(NW * 64) void scan_fwd_kernel(ScanArgs p) {
     const int64_t d0 = (int64_t)g * p.per + ch0;
     const int nch = p.per - ch0 < 16 * C ? p.per - ch0 : 16 * C;
     const int nv = nch - cl * C < 0 ? 0 : nch - cl * C > C ? C : nch - cl * C;
-    const int64_t dl0 = d0 + cl * C;                // this lane's first channel
     const int64_t len = seq_len(p.lengths, b, p.T);
-    const bool vec = p.vec;
+    const bool whole = p.vec && nch == 16 * C;      // every lane reads and writes whole vectors
     float A2[S][C], skip[C], bias[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
+        const int64_t d = d0 + cl * C + c;
         const bool ok = c < nv;
-        skip[c] = ok && p.skip ? p.skip[dl0 + c] : 0.f;
-        bias[c] = ok && p.delta_bias ? p.delta_bias[dl0 + c] : 0.f;
+        skip[c] = ok && p.skip ? p.skip[d] : 0.f;
+        bias[c] = ok && p.delta_bias ? p.delta_bias[d] : 0.f;
 #pragma unroll
         for (int s = 0; s < S; ++s) {
             const int n = sg * S + s;
-            A2[s][c] = ok && n < p.N ? p.A[(dl0 + c) * p.N + n] * LOG2E : 0.f;
+            A2[s][c] = ok && n < p.N ? p.A[d * p.N + n] * LOG2E : 0.f;
         }
     }
     // folded states: thread tid carries positions tid, tid + NT, ... of the tile
     float carry[FPT];
-    int64_t st_off[FPT];  // offset in (D, N), or -1
+    int st_off[FPT];  // offset from the tile's first state, or -1
+    const int64_t st_base = b * p.D * p.N + d0 * p.N;
 #pragma unroll
     for (int f = 0; f < FPT; ++f) {
         const int i = tid + f * NT;
         int ln, e;
         LV::where(i < E ? i : 0, &ln, &e);
         const int n = (ln >> 4) * S + e % S, ch = (ln & 15) * C + e / S;
-        st_off[f] = i < E && n < p.N && ch < nch ? (d0 + ch) * p.N + n : -1;
-        carry[f] = st_off[f] >= 0 && p.h0 ? p.h0[b * p.D * p.N + st_off[f]] : 0.f;
+        st_off[f] = i < E && n < p.N && ch < nch ? ch * (int)p.N + n : -1;
+        carry[f] = st_off[f] >= 0 && p.h0 ? p.h0[st_base + st_off[f]] : 0.f;
     }
-    const T *u = static_cast<const T *>(p.u) + b * p.T * p.D + dl0;
-    const T *delta = static_cast<const T *>(p.delta) + b * p.T * p.D + dl0;
-    const T *z = p.z ? static_cast<const T *>(p.z) + b * p.T * p.D + dl0 : nullptr;
-    const T *Bm = static_cast<const T *>(p.Bm) + (b * p.T * p.G + g) * p.N;
-    const T *Cm = static_cast<const T *>(p.Cm) + (b * p.T * p.G + g) * p.N;
-    T *y = static_cast<T *>(p.y) + b * p.T * p.D + dl0;
-    const int64_t brow = (int64_t)p.G * p.N;
-    const int64_t n_state_blocks = p.states ? (p.T + scan_block_of<S>() - 1) / scan_block_of<S>() : 0;
+    // a lane's rows: steps sg, 4 + sg, ... of the wave's, as byte offsets from the wave's first
+    const uint32_t row = (uint32_t)(p.D * (int64_t)sizeof(T));
+    uint32_t voff[J], boff[BPL];
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+        voff[j] = nv > 0 ? (uint32_t)(4 * j + sg) * row + (uint32_t)(cl * C * sizeof(T)) : NO_CHANNEL;
+    const int64_t row0 = b * p.T * p.D + d0;
+    const int64_t brow = (int64_t)p.G * p.N, b0 = (b * p.T * p.G + g) * p.N;
+#pragma unroll
+    for (int i = 0; i < BPL; ++i) {
+        const int q = lane + 64 * i, t = q / NP, n = q % NP;
+        boff[i] = q < L * NP && n < p.N ? (uint32_t)((t * brow + n) * (int64_t)sizeof(T)) : NO_CHANNEL;
+    }
+    raw_t ur[J], dr[J], zr[J];
+    one_t br[BPL], cr[BPL];
 
+    // the wave's rows of the block in which its steps start at t0
+    const auto load = [&](int64_t t0) {
+        const int64_t left = steps_left<L>(t0, len);
+        load_rows<T, C, J>(make_rows(static_cast<const T *>(p.u) + row0 + t0 * p.D, left * row), voff, nv, whole, ur);
+        load_rows<T, C, J>(make_rows(static_cast<const T *>(p.delta) + row0 + t0 * p.D, left * row), voff, nv, whole,
+                           dr);
+        if (p.z)
+            load_rows<T, C, J>(make_rows(static_cast<const T *>(p.z) + row0 + t0 * p.D, left * row), voff, nv, whole,
+                               zr);
+        const rsrc_t rb = make_rows(static_cast<const T *>(p.Bm) + b0 + t0 * brow, left * brow * (int64_t)sizeof(T));
+        const rsrc_t rc = make_rows(static_cast<const T *>(p.Cm) + b0 + t0 * brow, left * brow * (int64_t)sizeof(T));
+#pragma unroll
+        for (int i = 0; i < BPL; ++i) {
+            br[i] = buf_read<T, 1>(rb, boff[i]);
+            cr[i] = buf_read<T, 1>(rc, boff[i]);
+        }
+    };
+
+    load((int64_t)wave * L);
     for (int64_t tb = 0; tb < p.T; tb += NW * L) {
         const int64_t t0 = tb + wave * L;
+        const int left = steps_left<L>(t0, len);
         // this wave's rows: dl and dl u by the lanes that own them
-        float uu[J][C], zz[J][C];
+        raw_t uk[J], zk[J];
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-            const int64_t t = t0 + 4 * j + sg;
-            const int n_ok = t < len ? nv : 0;
-            float dd[C];
-            load_ch<T, C>(u + t * p.D, n_ok, vec, uu[j]);
-            load_ch<T, C>(delta + t * p.D, n_ok, vec, dd);
-            if (z) load_ch<T, C>(z + t * p.D, n_ok, vec, zz[j]);
-            float o[2 * C];
+            float uu[C], dd[C], o[2 * C];
+            PC::unpack(ur[j], uu);
+            PC::unpack(dr[j], dd);
+            uk[j] = ur[j];
+            zk[j] = zr[j];
+            const bool in = 4 * j + sg < left;
 #pragma unroll
             for (int c = 0; c < C; ++c) {
-                float unused;
-                const float r = gate_rate(dd[c] + bias[c], p.softplus, &unused);
-                o[c] = c < n_ok ? r : 0.f;
-                o[C + c] = o[c] * uu[j][c];
+                const float r = gate_rate(dd[c] + bias[c], p.softplus, nullptr);
+                o[c] = in ? r : 0.f;
+                o[C + c] = o[c] * uu[c];
             }
 #pragma unroll
             for (int i = 0; i < 2 * C; ++i) sm_x[wave][4 * j + sg][cl][i] = o[i];
@@ -98,15 +131,13 @@ __global__ __launch_bounds__(NW * 64) void scan_fwd_kernel(ScanArgs p) {
 #pragma unroll
         for (int i = 0; i < BPL; ++i) {
             const int q = lane + 64 * i, t = q / NP, n = q % NP;
-            const bool ok = q < L * NP && t0 + t < len && n < p.N;
-            const float bv = ok ? ld1(Bm + (t0 + t) * brow + n) : 0.f;
-            const float cv = ok ? ld1(Cm + (t0 + t) * brow + n) : 0.f;
-            if (q < L * NP) {
-                sm_b[wave][0][t][n] = bv;
-                sm_b[wave][1][t][n] = cv;
+            if (L * NP % 64 == 0 || q < L * NP) {
+                Pack<T, 1>::unpack(br[i], &sm_b[wave][n][t]);
+                Pack<T, 1>::unpack(cr[i], &sm_c[wave][t][n]);
             }
         }
-        wave_lds_fence();
+        if (tb + NW * L < p.T) load(t0 + NW * L);
+        wave_lds_sync();
         // the wave's steps from a zero state
         float a[L][S][C], h[S][C], yl[L][C], sum[C];
 #pragma unroll
@@ -115,23 +146,35 @@ __global__ __launch_bounds__(NW * 64) void scan_fwd_kernel(ScanArgs p) {
 #pragma unroll
             for (int s = 0; s < S; ++s) h[s][c] = 0.f;
         }
+        const int n0 = QR::first(lane);
 #pragma unroll
-        for (int t = 0; t < L; ++t) {
-            float dx[2 * C], bt[S], ct[S];
-            __builtin_amdgcn_sched_barrier(0);
-            lds_read<2 * C>(sm_x[wave][t][cl], dx);
-            lds_read<S>(&sm_b[wave][0][t][sg * S], bt);
-            lds_read<S>(&sm_b[wave][1][t][sg * S], ct);
+        for (int tq = 0; tq < L; tq += 4) {
+            float bq[NB][4];
 #pragma unroll
-            for (int c = 0; c < C; ++c) {
-                sum[c] += dx[c];
-                yl[t][c] = 0.f;
+            for (int i = 0; i < NB; ++i) lds_read<4>(&sm_b[wave][n0 + 4 * i][tq], bq[i]);
 #pragma unroll
-                for (int s = 0; s < S; ++s) {
-                    a[t][s][c] = __builtin_amdgcn_exp2f(dx[c] * A2[s][c]);
-                    h[s][c] = fmaf(a[t][s][c], h[s][c], dx[C + c] * bt[s]);
-                    yl[t][c] = fmaf(ct[s], h[s][c], yl[t][c]);
-                }
+            for (int k = 0; k < 4; ++k) {
+                const int t = tq + k;
+                __builtin_amdgcn_sched_barrier(0);
+                float dx[2 * C], bt[NB], ct[S];
+                lds_read<2 * C>(sm_x[wave][t][cl], dx);
+                lds_read<S>(&sm_c[wave][t][sg * S], ct);
+#pragma unroll
+                for (int i = 0; i < NB; ++i) bt[i] = bq[i][k];
+#pragma unroll
+                for (int c = 0; c < C; ++c) { sum[c] += dx[c]; yl[t][c] = 0.f; }
+                for_each<S>([&](auto si) {
+                    constexpr int s = decltype(si)::value;
+                    const float bs = QR::template get<s>(bt);
+#pragma unroll
+                    for (int c = 0; c < C; ++c) {
+                        a[t][s][c] = __builtin_amdgcn_exp2f(dx[c] * A2[s][c]);
+                        const float x = bs * dx[C + c];
+                        h[s][c] = t == 0 ? x : fmaf(a[t][s][c], h[s][c], x);
+                        yl[t][c] = fmaf(ct[s], h[s][c], yl[t][c]);
+                    }
+                });
+                pin(yl[t]);
             }
         }
         float hv[EL], pv[EL];
@@ -144,31 +187,39 @@ __global__ __launch_bounds__(NW * 64) void scan_fwd_kernel(ScanArgs p) {
             }
         LV::write(sm_s[wave], lane, hv);
         LV::write(sm_p[wave], lane, pv);
-        __syncthreads();
+        wg_lds_sync();
 #pragma unroll
         for (int f = 0; f < FPT; ++f) {
             const int i = tid + f * NT;
             if (i < E) {
-                float c = carry[f];
+                float c = carry[f], sv[NW], pw[NW];
 #pragma unroll
                 for (int w = 0; w < NW; ++w) {
-                    if (p.states && st_off[f] >= 0 && tb + w * L < p.T && (tb + w * L) % scan_block_of<S>() == 0)
-                        p.states[(b * n_state_blocks + (tb + w * L) / scan_block_of<S>()) * p.D * p.N + st_off[f]] = c;
-                    const float s = sm_s[w][i];
+                    sv[w] = sm_s[w][i];
+                    pw[w] = sm_p[w][i];
+                }
+#pragma unroll
+                for (int w = 0; w < NW; ++w) {
+                    if ((w * L) % scan_block_of<S>() % (NW * L) == 0 && (tb + w * L) % scan_block_of<S>() == 0 &&
+                        p.states && st_off[f] >= 0 && tb + w * L < p.T) {
+                        const int64_t blk = (tb + w * L) / scan_block_of<S>();
+                        const int64_t n_blk = (p.T + scan_block_of<S>() - 1) / scan_block_of<S>();
+                        p.states[(b * n_blk + blk) * p.D * p.N + d0 * p.N + st_off[f]] = c;
+                    }
                     sm_s[w][i] = c;
-                    c = fmaf(sm_p[w][i], c, s);
+                    c = fmaf(pw[w], c, sv[w]);
                 }
                 carry[f] = c;
             }
         }
-        __syncthreads();
+        wg_lds_sync();
         // the state that entered the wave, carried through its gates
         LV::read(sm_s[wave], lane, hv);
 #pragma unroll
         for (int t = 0; t < L; ++t) {
-            float ct[S];
             __builtin_amdgcn_sched_barrier(0);
-            lds_read<S>(&sm_b[wave][1][t][sg * S], ct);
+            float ct[S];
+            lds_read<S>(&sm_c[wave][t][sg * S], ct);
 #pragma unroll
             for (int c = 0; c < C; ++c)
 #pragma unroll
@@ -176,28 +227,30 @@ __global__ __launch_bounds__(NW * 64) void scan_fwd_kernel(ScanArgs p) {
                     hv[c * S + s] *= a[t][s][c];
                     yl[t][c] = fmaf(ct[s], hv[c * S + s], yl[t][c]);
                 }
+            pin(yl[t]);
         }
         float out[J][C];
         sg_join<L, C>(yl, out);
+        char *y = reinterpret_cast<char *>(static_cast<T *>(p.y) + row0 + t0 * p.D);
+        const int rows = steps_left<L>(t0, p.T);
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-            const int64_t t = t0 + 4 * j + sg;
-            if (t < p.T) {
-                float o[C];
+            float uu[C], zz[C], o[C];
+            PC::unpack(uk[j], uu);
+            PC::unpack(zk[j], zz);
 #pragma unroll
-                for (int c = 0; c < C; ++c) {
-                    o[c] = fmaf(skip[c], uu[j][c], out[j][c]);
-                    if (z) o[c] *= silu(zz[j][c]);
-                    if (t >= len) o[c] = 0.f;
-                }
-                store_ch<T, C>(y + t * p.D, nv, vec, o);
+            for (int c = 0; c < C; ++c) {
+                o[c] = fmaf(skip[c], uu[c], out[j][c]);
+                if (p.z) o[c] *= silu(zz[c]);
+                if (4 * j + sg >= left) o[c] = 0.f;
             }
+            if (4 * j + sg < rows) store_ch<T, C>(y + voff[j], nv, whole, o);
         }
     }
     if (p.hT)
 #pragma unroll
         for (int f = 0; f < FPT; ++f)
-            if (st_off[f] >= 0) p.hT[b * p.D * p.N + st_off[f]] = carry[f];
+            if (st_off[f] >= 0) p.hT[st_base + st_off[f]] = carry[f];
 }
 
 // One token: a lane owns up to four states of a channel, LQ lanes a channel.
@@ -215,8 +268,7 @@ __global__ __launch_bounds__(256) void scan_step_kernel(ScanArgs p, int lq, int6
         d = chan - b * p.D;
         const float uu = ld1(static_cast<const T *>(p.u) + chan);
         const float raw = ld1(static_cast<const T *>(p.delta) + chan) + (p.delta_bias ? p.delta_bias[d] : 0.f);
-        float unused;
-        const float dl = gate_rate(raw, p.softplus, &unused);
+        const float dl = gate_rate(raw, p.softplus, nullptr);
         const float x = dl * uu;
         const int64_t brow = (b * p.G + d / p.per) * p.N;
 #pragma unroll
@@ -238,16 +290,34 @@ __global__ __launch_bounds__(256) void scan_step_kernel(ScanArgs p, int lq, int6
     }
 }
 
-template <typename T, int S>
-mi_status launch_fwd(ScanArgs a, hipStream_t s) {
-    using TL = ScanTile<S>;
-    a.tiles = (a.per + 16 * TL::C - 1) / (16 * TL::C);
+template <typename T, int S, int C, int L, int NW, int WPS>
+mi_status launch_tile(ScanArgs a, hipStream_t s) {
+    a.tiles = (a.per + 16 * C - 1) / (16 * C);
     int64_t items;
     if (!mul_ok(a.B, a.G, a.tiles, 1, &items) || items > 0x7ffffff0) return MI_ERR_UNSUPPORTED;
     a.n_items = (int)items;
-    hipLaunchKernelGGL((scan_fwd_kernel<T, S, TL::C, TL::L, SCAN_NW>), dim3(xcd_grid(a.n_items)), dim3(SCAN_NW * 64),
-                       0, s, a);
+    hipLaunchKernelGGL((scan_fwd_kernel<T, S, C, L, NW, WPS>), dim3(xcd_grid(a.n_items)), dim3(NW * 64), 0, s, a);
     return launch_status();
+}
+
+// Tile of a call, by the number of workgroups that its wide tiles make.
+//  - 768 or more (three a CU): workgroups of 4 waves at 3 waves a SIMD, which
+//    overlap each other's folds; B = 8, T = 4096, D = 4096, N = 16, bf16 (1024):
+//    744 us, against 892 with 8 waves.
+//  - fewer: 8 waves, so that a workgroup a CU still fills half of it; B = 2, T =
+//    4096, D = 4096 with z (256): 237 us, against 349 with 4 waves.
+//  - fewer than 256: narrow tiles (one channel a lane) of 16 waves: twice the
+//    workgroups and four times the waves; B = 1, T = 8192, D = 4096 with z (128):
+//    251 us, against 456 with wide tiles of 8 waves.  At 256 both take the same
+//    (249 and 237).
+template <typename T, int S>
+mi_status launch_fwd(const ScanArgs &a, hipStream_t s) {
+    constexpr int C = ScanTile<S>::C, L = ScanTile<S>::L;
+    constexpr int LN = S >= 8 ? 4 : S >= 2 ? 8 : 16;  // at most 32 gates a lane: 128 registers (64 gates for S = 16)
+    const int64_t n = a.B * a.G * ((a.per + 16 * C - 1) / (16 * C));
+    if (n >= 768) return launch_tile<T, S, C, L, 4, S == 2 || S == 16 ? 2 : 3>(a, s);
+    if (n >= 256 || S == 16) return launch_tile<T, S, C, L, 8, 2>(a, s);
+    return launch_tile<T, S, 1, LN, S == 16 ? 8 : 16, S == 16 ? 2 : 4>(a, s);
 }
 template <typename T>
 mi_status launch_fwd_t(const ScanArgs &a, hipStream_t s) {
@@ -310,7 +380,7 @@ mi_status mi_selective_scan_fwd(const void *u, const void *delta, const float *A
     a.u = u; a.delta = delta; a.z = z; a.Bm = Bm; a.Cm = Cm; a.A = A; a.skip = skip; a.delta_bias = delta_bias;
     a.h0 = h0; a.lengths = lengths; a.y = y; a.hT = hT; a.states = states;
     a.B = B; a.T = T; a.D = D; a.N = N; a.softplus = softplus_on != 0;
-    if (D / G > 0x40000000 || G > 0x40000000) return MI_ERR_UNSUPPORTED;
+    if (D > SCAN_MAX_D || G * N > SCAN_MAX_D) return MI_ERR_UNSUPPORTED;
     a.G = (int)G; a.per = (int)(D / G);
     a.vec = scan_vec(a, dt);
     if (dt == MI_F32) return launch_fwd_t<float>(a, stream);
@@ -336,7 +406,7 @@ mi_status mi_selective_scan_step(const void *u, const void *delta, const float *
     a.u = u; a.delta = delta; a.z = z; a.Bm = Bm; a.Cm = Cm; a.A = A; a.skip = skip; a.delta_bias = delta_bias;
     a.h0 = h; a.y = y; a.hT = h_out;
     a.B = B; a.T = 1; a.D = D; a.N = N; a.softplus = softplus_on != 0;
-    if (D / G > 0x40000000 || G > 0x40000000) return MI_ERR_UNSUPPORTED;
+    if (D > SCAN_MAX_D || G * N > SCAN_MAX_D) return MI_ERR_UNSUPPORTED;
     a.G = (int)G; a.per = (int)(D / G);
     int lq = 1;
     while (lq * 4 < N) lq *= 2;

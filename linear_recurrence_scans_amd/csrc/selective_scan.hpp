@@ -52,6 +52,9 @@ template <> struct ScanTile<8> { static constexpr int C = 1, L = 8; };
 template <> struct ScanTile<16> { static constexpr int C = 1, L = 4; };
 
 constexpr int SCAN_NW = 8;  // waves a workgroup
+// Rows inside a block are addressed with 32-bit byte offsets: 16 rows of D
+// (or G N) 4-byte values stay below 2^31.
+constexpr int64_t SCAN_MAX_D = 1 << 24;
 
 inline int scan_s(int64_t N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }
 
@@ -96,54 +99,131 @@ __device__ __forceinline__ float swap_add16(float a, float b) {
     const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
+// Joins four consecutive steps.
+template <int C>
+__device__ __forceinline__ void sg_join4(const float (&y0)[C], const float (&y1)[C], const float (&y2)[C],
+                                         const float (&y3)[C], float (&out)[C]) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) out[c] = swap_add16(swap_add32(y0[c], y2[c]), swap_add32(y1[c], y3[c]));
+}
 template <int L, int C>
 __device__ __forceinline__ void sg_join(const float (&y)[L][C], float (&out)[L / 4][C]) {
 #pragma unroll
-    for (int j = 0; j < L / 4; ++j)
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-            out[j][c] = swap_add16(swap_add32(y[4 * j][c], y[4 * j + 2][c]),
-                                   swap_add32(y[4 * j + 1][c], y[4 * j + 3][c]));
+    for (int j = 0; j < L / 4; ++j) sg_join4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3], out[j]);
 }
 
-// C consecutive channels of a row; nv of them exist (0: none).  Missing ones
-// are zero.
-template <typename T, int C>
-__device__ __forceinline__ void load_ch(const T *p, int nv, bool vec, float (&f)[C]) {
+// Row access.  A wave's block of rows is one buffer descriptor whose size ends
+// after the last step that exists, so a lane needs 32-bit offsets only, and
+// steps past a sequence's end read as zero without a select; so do channels past
+// the tile's end, whose offset is NO_CHANNEL.  Rows are read with the default
+// cache policy: a 128-byte line holds the channels of two to four tiles.
+constexpr uint32_t NO_CHANNEL = 0x7ffffff0u;
+
+template <typename T, int N>
+__device__ __forceinline__ typename Pack<T, N>::raw_t buf_read(rsrc_t r, uint32_t voff) {
+    using raw_t = typename Pack<T, N>::raw_t;
+    constexpr int BYTES = (int)sizeof(T) * N;
+    if constexpr (BYTES == 8) return __builtin_bit_cast(raw_t, __builtin_amdgcn_raw_buffer_load_b64(r, voff, 0, 0));
+    else if constexpr (BYTES == 4) return __builtin_bit_cast(raw_t, __builtin_amdgcn_raw_buffer_load_b32(r, voff, 0, 0));
+    else return __builtin_bit_cast(raw_t, __builtin_amdgcn_raw_buffer_load_b16(r, voff, 0, 0));
+}
+
+// The C channels of J rows at offsets voff: whole vectors, or single elements
+// of which the first nv exist.
+template <typename T, int C, int J>
+__device__ __forceinline__ void load_rows(rsrc_t r, const uint32_t (&voff)[J], int nv, bool whole,
+                                          typename Pack<T, C>::raw_t (&raw)[J]) {
+    if (whole) {
 #pragma unroll
-    for (int c = 0; c < C; ++c) f[c] = 0.f;
-    if (nv == C && vec) {
-        Pack<T, C>::unpack(load_vec<T, C>(p), f);
+        for (int j = 0; j < J; ++j) raw[j] = buf_read<T, C>(r, voff[j]);
     } else {
 #pragma unroll
-        for (int c = 0; c < C; ++c)
-            if (c < nv) f[c] = ld1(p + c);
+        for (int j = 0; j < J; ++j) {
+            float f[C];
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                Pack<T, 1>::unpack(buf_read<T, 1>(r, c < nv ? voff[j] + c * (uint32_t)sizeof(T) : NO_CHANNEL), f + c);
+            raw[j] = Pack<T, C>::pack(f);
+        }
     }
 }
+
+// The C channels of a lane's row, of which the first nv exist.
 template <typename T, int C>
-__device__ __forceinline__ void store_ch(T *p, int nv, bool vec, const float (&f)[C]) {
-    if (nv == C && vec) {
+__device__ __forceinline__ void store_ch(char *p, int nv, bool whole, const float (&f)[C]) {
+    if (whole) {
         *reinterpret_cast<typename Pack<T, C>::raw_t *>(p) = Pack<T, C>::pack(f);
     } else {
 #pragma unroll
         for (int c = 0; c < C; ++c)
-            if (c < nv) st1(p + c, f[c]);
+            if (c < nv) st1(reinterpret_cast<T *>(p) + c, f[c]);
     }
 }
 
-// dl = softplus(raw) or raw, with its derivative.
-__device__ __forceinline__ float gate_rate(float raw, int use_softplus, float *deriv) {
-    float sig;
-    const float sp = softplus(raw, &sig);
-    *deriv = use_softplus ? sig : 1.f;
-    return use_softplus ? sp : raw;
+// Steps of [t0, t0 + L) before `end`.
+template <int L>
+__device__ __forceinline__ int steps_left(int64_t t0, int64_t end) {
+    return t0 >= end ? 0 : end - t0 < L ? (int)(end - t0) : L;
 }
 
-// Wave-level LDS ordering: data exchanged inside one wave needs its own LDS
-// operations done, no workgroup barrier.
-__device__ __forceinline__ void wave_lds_fence() {
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+// dl = softplus(raw) or raw, with its derivative where `deriv` is not null.
+__device__ __forceinline__ float gate_rate(float raw, int use_softplus, float *deriv) {
+    if (use_softplus) return softplus(raw, deriv);
+    if (deriv != nullptr) *deriv = 1.f;
+    return raw;
+}
+
+// LDS ordering.  Fences of the local address space make the compiler and the
+// LDS queue keep the order without waiting for global loads in flight, which a
+// __syncthreads() would drain.  wave_lds_sync: data exchanged inside one wave;
+// wg_lds_sync: inside the workgroup.
+__device__ __forceinline__ void wave_lds_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
     __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+__device__ __forceinline__ void wg_lds_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// Bm rows.  All lanes of a quad need the same S values of a row (their states'),
+// so a lane holds every fourth only: register i of lane l is state 4 i + (l & 3)
+// of its S (l & 1 for S = 2), and a multiplication takes state s from its quad
+// with a DPP operand, at no extra instruction.  Held as [state][step] in LDS,
+// four steps come with one 16-byte read.  (fma has no DPP form here, so Cm rows
+// are read whole.)
+template <int S>
+struct QuadRow {
+    static constexpr int NB = (S + 3) / 4, MASK = S >= 4 ? 3 : S - 1;
+    static __device__ __forceinline__ int first(int lane) { return (lane >> 4) * S + (lane & MASK); }
+    template <int s>
+    static __device__ __forceinline__ float get(const float (&r)[NB]) {
+        constexpr int q = s & 3;
+        if constexpr (S == 1) return r[0];
+        else return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, r[s / 4]), q * 0x55, 0xf,
+                                                                       0xf, true));
+    }
+};
+
+// for_each<N>(f): f(Num<0>()), ..., f(Num<N - 1>()): loops whose index is a
+// constant expression.
+template <int K> struct Num { static constexpr int value = K; };
+template <int N, int I = 0, class F>
+__device__ __forceinline__ void for_each(F &&f) {
+    if constexpr (I < N) {
+        f(Num<I>());
+        for_each<N, I + 1>(f);
+    }
+}
+
+// Pins C values to this point of the program: the compiler otherwise sinks sums
+// that are needed later to their use and keeps all their terms in registers.
+template <int C>
+__device__ __forceinline__ void pin(float (&v)[C]) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) asm volatile("" : "+v"(v[c]));
 }
 
 // N consecutive floats of LDS as 16-, 8- or 4-byte accesses.
@@ -169,25 +249,23 @@ __device__ __forceinline__ void lds_read(const float *p, float (&f)[N]) {
 template <int EL>
 struct LaneVec {
     static constexpr int V = EL < 4 ? EL : 4;
+    static_assert(V == 1 || V == 2 || V == 4, "elements a lane");
     static __device__ __forceinline__ void write(float *p, int lane, const float (&f)[EL]) {
 #pragma unroll
         for (int g = 0; g < EL / V; ++g) {
             float *q = p + (g * 64 + lane) * V;
             if constexpr (V == 4) *reinterpret_cast<f32x4 *>(q) = f32x4{f[4 * g], f[4 * g + 1], f[4 * g + 2], f[4 * g + 3]};
-            else *reinterpret_cast<f32x2 *>(q) = f32x2{f[2 * g], f[2 * g + 1]};
+            else if constexpr (V == 2) *reinterpret_cast<f32x2 *>(q) = f32x2{f[2 * g], f[2 * g + 1]};
+            else *q = f[g];
         }
     }
     static __device__ __forceinline__ void read(const float *p, int lane, float (&f)[EL]) {
 #pragma unroll
         for (int g = 0; g < EL / V; ++g) {
-            const float *q = p + (g * 64 + lane) * V;
-            if constexpr (V == 4) {
-                const f32x4 r = *reinterpret_cast<const f32x4 *>(q);
-                f[4 * g] = r.x; f[4 * g + 1] = r.y; f[4 * g + 2] = r.z; f[4 * g + 3] = r.w;
-            } else {
-                const f32x2 r = *reinterpret_cast<const f32x2 *>(q);
-                f[2 * g] = r.x; f[2 * g + 1] = r.y;
-            }
+            float v[V];
+            lds_read<V>(p + (g * 64 + lane) * V, v);
+#pragma unroll
+            for (int i = 0; i < V; ++i) f[g * V + i] = v[i];
         }
     }
     // (lane, element) of linear position i

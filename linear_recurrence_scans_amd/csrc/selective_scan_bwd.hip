@@ -25,7 +25,10 @@ struct BwdShared {
     static constexpr int E = S * C * 64, TR = join_steps(S, L), V = TR * S, ROW = 4 * V + 4;
     float x[NW][L][16][2 * C];   // dl, dl u
     float ds[NW][L][16][C];
-    float b[NW][2][L][4 * S];    // Bm, Cm
+    static constexpr bool BY_STATE = S < 16;  // room for both orders of Bm
+    float bt[NW][BY_STATE ? 4 * S : 1][L + 4];  // Bm by state
+    float b[NW][L][4 * S];       // Bm by step
+    float c[NW][L][4 * S];       // Cm by step
     float s[NW][E], p[NW][E], r[NW][E];
     float red[NW][16][ROW];      // values to sum over the channel lanes; rows four banks apart
 };
@@ -49,13 +52,19 @@ __device__ __forceinline__ void join_channels(const float (*red)[ROW], int lane,
     }
 }
 
-template <typename T, int S, int C, int L, int NW>
-__global__ __launch_bounds__(NW * 64) void scan_bwd_kernel(ScanArgs p) {
+template <typename T, int S, int C, int L, int NW, bool GATED>
+__global__ __launch_bounds__(NW * 64, 2) void scan_bwd_kernel(ScanArgs p) {
     constexpr int EL = S * C, J = L / 4, NP = 4 * S;
     constexpr int E = EL * 64, NT = NW * 64, FPT = (E + NT - 1) / NT, BPL = (L * NP + 63) / 64;
     using LV = LaneVec<EL>;
+    using QR = QuadRow<S>;
+    constexpr int NB = QR::NB;
+    using PC = Pack<T, C>;
+    using raw_t = typename PC::raw_t;
+    using one_t = typename Pack<T, 1>::raw_t;
     using SH = BwdShared<S, C, L, NW>;
     constexpr int TR = SH::TR, V = SH::V;
+    constexpr bool BY_STATE = SH::BY_STATE;
     extern __shared__ __align__(16) char smem[];
     SH &sm = *reinterpret_cast<SH *>(smem);
     const int item = xcd_item(p.n_items);
@@ -70,88 +79,119 @@ __global__ __launch_bounds__(NW * 64) void scan_bwd_kernel(ScanArgs p) {
     const int64_t d0 = (int64_t)g * p.per + ch0;
     const int nch = p.per - ch0 < 16 * C ? p.per - ch0 : 16 * C;
     const int nv = nch - cl * C < 0 ? 0 : nch - cl * C > C ? C : nch - cl * C;
-    const int64_t dl0 = d0 + cl * C;
     const int64_t len = seq_len(p.lengths, b, p.T);
-    const bool vec = p.vec;
+    const bool whole = p.vec && nch == 16 * C;
     float A2[S][C], skip[C], bias[C], dA[S][C], dskip[C], dbias[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
+        const int64_t d = d0 + cl * C + c;
         const bool ok = c < nv;
-        skip[c] = ok && p.skip ? p.skip[dl0 + c] : 0.f;
-        bias[c] = ok && p.delta_bias ? p.delta_bias[dl0 + c] : 0.f;
+        skip[c] = ok && p.skip ? p.skip[d] : 0.f;
+        bias[c] = ok && p.delta_bias ? p.delta_bias[d] : 0.f;
         dskip[c] = dbias[c] = 0.f;
 #pragma unroll
         for (int s = 0; s < S; ++s) {
             const int n = sg * S + s;
-            A2[s][c] = ok && n < p.N ? p.A[(dl0 + c) * p.N + n] * LOG2E : 0.f;
+            A2[s][c] = ok && n < p.N ? p.A[d * p.N + n] * LOG2E : 0.f;
             dA[s][c] = 0.f;
         }
     }
-    float carry[FPT];     // gradient that enters the block from its right
-    int64_t st_off[FPT];  // offset in (D, N), or -1
+    float carry[FPT], h0[FPT];  // gradient that enters the block from its right; state before the block
+    int st_off[FPT];            // offset from the tile's first state, or -1
+    const int64_t st_base = b * p.D * p.N + d0 * p.N;
 #pragma unroll
     for (int f = 0; f < FPT; ++f) {
         const int i = tid + f * NT;
         int ln, e;
         LV::where(i < E ? i : 0, &ln, &e);
         const int n = (ln >> 4) * S + e % S, ch = (ln & 15) * C + e / S;
-        st_off[f] = i < E && n < p.N && ch < nch ? (d0 + ch) * p.N + n : -1;
-        carry[f] = st_off[f] >= 0 && p.dhT ? p.dhT[b * p.D * p.N + st_off[f]] : 0.f;
+        st_off[f] = i < E && n < p.N && ch < nch ? ch * (int)p.N + n : -1;
+        carry[f] = st_off[f] >= 0 && p.dhT ? p.dhT[st_base + st_off[f]] : 0.f;
     }
-    const int64_t row0 = b * p.T * p.D + dl0;
-    const T *u = static_cast<const T *>(p.u) + row0;
-    const T *delta = static_cast<const T *>(p.delta) + row0;
-    const T *dy = static_cast<const T *>(p.dy) + row0;
-    const T *z = p.z ? static_cast<const T *>(p.z) + row0 : nullptr;
-    const T *Bm = static_cast<const T *>(p.Bm) + (b * p.T * p.G + g) * p.N;
-    const T *Cm = static_cast<const T *>(p.Cm) + (b * p.T * p.G + g) * p.N;
-    T *du = static_cast<T *>(p.du) + row0;
-    T *ddelta = static_cast<T *>(p.ddelta) + row0;
-    T *dz = p.z ? static_cast<T *>(p.dz) + row0 : nullptr;
-    const int64_t brow = (int64_t)p.G * p.N;
+    const uint32_t row = (uint32_t)(p.D * (int64_t)sizeof(T));
+    uint32_t voff[J], boff[BPL];
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+        voff[j] = nv > 0 ? (uint32_t)(4 * j + sg) * row + (uint32_t)(cl * C * sizeof(T)) : NO_CHANNEL;
+    const int64_t row0 = b * p.T * p.D + d0;
+    const int64_t brow = (int64_t)p.G * p.N, b0 = (b * p.T * p.G + g) * p.N;
+#pragma unroll
+    for (int i = 0; i < BPL; ++i) {
+        const int q = lane + 64 * i, t = q / NP, n = q % NP;
+        boff[i] = q < L * NP && n < p.N ? (uint32_t)((t * brow + n) * (int64_t)sizeof(T)) : NO_CHANNEL;
+    }
     const int64_t bc = p.B * p.T * brow;  // floats of dBm
-    float *part_b = p.part_bc + (int64_t)tile * 2 * bc + (b * p.T * p.G + g) * p.N;
+    float *part_b = p.part_bc + (int64_t)tile * 2 * bc + b0;
     float *part_c = part_b + bc;
     const int64_t n_blk = (p.T + NW * L - 1) / (NW * L);
+    const int n0 = QR::first(lane);
+    raw_t ur[J], dr[J], zr[J], gr[J];
+    one_t br[BPL], cr[BPL];
 
+    // this wave's rows of a block, and the state before it
+    const auto load = [&](int64_t blk) {
+        const int64_t t0 = blk * (NW * L) + wave * L, left = steps_left<L>(t0, len);
+        load_rows<T, C, J>(make_rows(static_cast<const T *>(p.u) + row0 + t0 * p.D, left * row), voff, nv, whole, ur);
+        load_rows<T, C, J>(make_rows(static_cast<const T *>(p.delta) + row0 + t0 * p.D, left * row), voff, nv, whole,
+                           dr);
+        load_rows<T, C, J>(make_rows(static_cast<const T *>(p.dy) + row0 + t0 * p.D, left * row), voff, nv, whole, gr);
+        if constexpr (GATED)
+            load_rows<T, C, J>(make_rows(static_cast<const T *>(p.z) + row0 + t0 * p.D, left * row), voff, nv, whole,
+                               zr);
+        const rsrc_t rb = make_rows(static_cast<const T *>(p.Bm) + b0 + t0 * brow, left * brow * (int64_t)sizeof(T));
+        const rsrc_t rc = make_rows(static_cast<const T *>(p.Cm) + b0 + t0 * brow, left * brow * (int64_t)sizeof(T));
+#pragma unroll
+        for (int i = 0; i < BPL; ++i) {
+            br[i] = buf_read<T, 1>(rb, boff[i]);
+            cr[i] = buf_read<T, 1>(rc, boff[i]);
+        }
+        const float *st = p.states + (b * n_blk + blk) * p.D * p.N + d0 * p.N;
+#pragma unroll
+        for (int f = 0; f < FPT; ++f) h0[f] = st_off[f] >= 0 ? st[st_off[f]] : 0.f;
+    };
+
+    if (n_blk > 0) load(n_blk - 1);
     for (int64_t blk = n_blk - 1; blk >= 0; --blk) {
         const int64_t t0 = blk * (NW * L) + wave * L;
-        float h0[FPT];  // the state before the block
-#pragma unroll
-        for (int f = 0; f < FPT; ++f)
-            h0[f] = st_off[f] >= 0 ? p.states[(b * n_blk + blk) * p.D * p.N + st_off[f]] : 0.f;
-        float uu[J][C], zz[J][C], gy[J][C], dl[J][C], der[J][C], ds[J][C];
+        const int left = steps_left<L>(t0, len), rows = steps_left<L>(t0, p.T);
+        raw_t uk[J], zk[J], gk[J];
+        float der[J][C], hin[FPT];
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-            const int64_t t = t0 + 4 * j + sg;
-            const int n_ok = t < len ? nv : 0;
-            float dd[C];
-            load_ch<T, C>(u + t * p.D, n_ok, vec, uu[j]);
-            load_ch<T, C>(delta + t * p.D, n_ok, vec, dd);
-            load_ch<T, C>(dy + t * p.D, n_ok, vec, gy[j]);
-            if (z) load_ch<T, C>(z + t * p.D, n_ok, vec, zz[j]);
+            float uu[C], dd[C], zz[C], gy[C];
+            PC::unpack(ur[j], uu);
+            PC::unpack(dr[j], dd);
+            PC::unpack(gr[j], gy);
+            if constexpr (GATED) PC::unpack(zr[j], zz);
+            uk[j] = ur[j];
+            gk[j] = gr[j];
+            if constexpr (GATED) zk[j] = zr[j];
+            const bool in = 4 * j + sg < left;
 #pragma unroll
             for (int c = 0; c < C; ++c) {
-                const float r = gate_rate(dd[c] + bias[c], p.softplus, &der[j][c]);
-                dl[j][c] = c < n_ok ? r : 0.f;
-                ds[j][c] = z ? gy[j][c] * silu(zz[j][c]) : gy[j][c];
-                sm.x[wave][4 * j + sg][cl][c] = dl[j][c];
-                sm.x[wave][4 * j + sg][cl][C + c] = dl[j][c] * uu[j][c];
-                sm.ds[wave][4 * j + sg][cl][c] = ds[j][c];
+                float r = gate_rate(dd[c] + bias[c], p.softplus, &der[j][c]);
+                r = in ? r : 0.f;
+                sm.x[wave][4 * j + sg][cl][c] = r;
+                sm.x[wave][4 * j + sg][cl][C + c] = r * uu[c];
+                if constexpr (GATED) gy[c] *= silu(zz[c]);
+                sm.ds[wave][4 * j + sg][cl][c] = gy[c];
             }
         }
 #pragma unroll
         for (int i = 0; i < BPL; ++i) {
             const int q = lane + 64 * i, t = q / NP, n = q % NP;
-            const bool ok = q < L * NP && t0 + t < len && n < p.N;
-            const float bv = ok ? ld1(Bm + (t0 + t) * brow + n) : 0.f;
-            const float cv = ok ? ld1(Cm + (t0 + t) * brow + n) : 0.f;
-            if (q < L * NP) {
-                sm.b[wave][0][t][n] = bv;
-                sm.b[wave][1][t][n] = cv;
+            if (L * NP % 64 == 0 || q < L * NP) {
+                float f;
+                Pack<T, 1>::unpack(br[i], &f);
+                if constexpr (BY_STATE) sm.bt[wave][n][t] = f;
+                sm.b[wave][t][n] = f;
+                Pack<T, 1>::unpack(cr[i], &sm.c[wave][t][n]);
             }
         }
-        wave_lds_fence();
+#pragma unroll
+        for (int f = 0; f < FPT; ++f) hin[f] = h0[f];
+        if (blk > 0) load(blk - 1);
+        wave_lds_sync();
         // local scans, forward and reverse
         float a[L][S][C];
         float hv[EL], gv[EL];
@@ -160,36 +200,53 @@ __global__ __launch_bounds__(NW * 64) void scan_bwd_kernel(ScanArgs p) {
 #pragma unroll
             for (int c = 0; c < C; ++c) sum[c] = 0.f;
 #pragma unroll
-            for (int e = 0; e < EL; ++e) hv[e] = gv[e] = 0.f;
+            for (int tq = 0; tq < L; tq += 4) {
+                float bq[NB][4];
 #pragma unroll
-            for (int t = 0; t < L; ++t) {
-                float x[2 * C], bt[S];
-                __builtin_amdgcn_sched_barrier(0);
-                lds_read<2 * C>(sm.x[wave][t][cl], x);
-                lds_read<S>(&sm.b[wave][0][t][sg * S], bt);
+                for (int i = 0; i < NB; ++i)
+                    if constexpr (BY_STATE) lds_read<4>(&sm.bt[wave][n0 + 4 * i][tq], bq[i]);
 #pragma unroll
-                for (int c = 0; c < C; ++c) {
-                    sum[c] += x[c];
+                for (int k = 0; k < 4; ++k) {
+                    const int t = tq + k;
+                    __builtin_amdgcn_sched_barrier(0);
+                    float x[2 * C], bt[NB], bw[S];
+                    lds_read<2 * C>(sm.x[wave][t][cl], x);
 #pragma unroll
-                    for (int s = 0; s < S; ++s) {
-                        a[t][s][c] = __builtin_amdgcn_exp2f(x[c] * A2[s][c]);
-                        hv[c * S + s] = fmaf(a[t][s][c], hv[c * S + s], x[C + c] * bt[s]);
-                    }
+                    for (int i = 0; i < NB; ++i)
+                        if constexpr (BY_STATE) bt[i] = bq[i][k];
+                    if constexpr (!BY_STATE) lds_read<S>(&sm.b[wave][t][sg * S], bw);
+#pragma unroll
+                    for (int c = 0; c < C; ++c) sum[c] += x[c];
+                    for_each<S>([&](auto si) {
+                        constexpr int s = decltype(si)::value;
+                        float bs;
+                        if constexpr (BY_STATE) bs = QR::template get<s>(bt);
+                        else bs = bw[s];
+#pragma unroll
+                        for (int c = 0; c < C; ++c) {
+                            a[t][s][c] = __builtin_amdgcn_exp2f(x[c] * A2[s][c]);
+                            const float xb = bs * x[C + c];
+                            hv[c * S + s] = t == 0 ? xb : fmaf(a[t][s][c], hv[c * S + s], xb);
+                        }
+                    });
+                    pin(hv);
                 }
             }
+            LV::write(sm.s[wave], lane, hv);
 #pragma unroll
             for (int t = L - 1; t >= 0; --t) {
-                float gs[C], ct[S];
                 __builtin_amdgcn_sched_barrier(0);
+                float gs[C], ct[S];
                 lds_read<C>(sm.ds[wave][t][cl], gs);
-                lds_read<S>(&sm.b[wave][1][t][sg * S], ct);
+                lds_read<S>(&sm.c[wave][t][sg * S], ct);
 #pragma unroll
                 for (int c = 0; c < C; ++c)
 #pragma unroll
                     for (int s = 0; s < S; ++s)
-                        gv[c * S + s] = a[t][s][c] * fmaf(ct[s], gs[c], gv[c * S + s]);
+                        gv[c * S + s] =
+                            a[t][s][c] * (t == L - 1 ? ct[s] * gs[c] : fmaf(ct[s], gs[c], gv[c * S + s]));
+                pin(gv);
             }
-            LV::write(sm.s[wave], lane, hv);
             LV::write(sm.r[wave], lane, gv);
 #pragma unroll
             for (int c = 0; c < C; ++c)
@@ -197,136 +254,155 @@ __global__ __launch_bounds__(NW * 64) void scan_bwd_kernel(ScanArgs p) {
                 for (int s = 0; s < S; ++s) hv[c * S + s] = __builtin_amdgcn_exp2f(sum[c] * A2[s][c]);
             LV::write(sm.p[wave], lane, hv);
         }
-        __syncthreads();
+        wg_lds_sync();
 #pragma unroll
         for (int f = 0; f < FPT; ++f) {
             const int i = tid + f * NT;
             if (i < E) {
-                float h = h0[f], gr = carry[f];
+                float h = hin[f], gc = carry[f], pw[NW], sv[NW], rv[NW];
 #pragma unroll
                 for (int w = 0; w < NW; ++w) {
-                    const float s = sm.s[w][i];
-                    sm.s[w][i] = h;
-                    h = fmaf(sm.p[w][i], h, s);
+                    pw[w] = sm.p[w][i];
+                    sv[w] = sm.s[w][i];
+                    rv[w] = sm.r[w][i];
                 }
 #pragma unroll
-                for (int w = NW - 1; w >= 0; --w) {
-                    const float r = sm.r[w][i];
-                    sm.r[w][i] = gr;
-                    gr = fmaf(sm.p[w][i], gr, r);
+                for (int w = 0; w < NW; ++w) {
+                    sm.s[w][i] = h;
+                    h = fmaf(pw[w], h, sv[w]);
+                    sm.r[NW - 1 - w][i] = gc;
+                    gc = fmaf(pw[NW - 1 - w], gc, rv[NW - 1 - w]);
                 }
-                carry[f] = gr;
+                carry[f] = gc;
             }
         }
-        __syncthreads();
+        wg_lds_sync();
         LV::read(sm.s[wave], lane, hv);
-        LV::read(sm.r[wave], lane, gv);
         // states: keep a_t h_{t-1}; s_t for the gate's gradient; dCm
-        float ah[L][S][C], sv[L][C];
+        float ah[L][S][C], sv[4][C], so[J][C];
 #pragma unroll
-        for (int t = 0; t < L; ++t) {
-            float x[2 * C], gs[C], bt[S], ct[S], dc[S];
-            __builtin_amdgcn_sched_barrier(0);
-            lds_read<2 * C>(sm.x[wave][t][cl], x);
-            lds_read<C>(sm.ds[wave][t][cl], gs);
-            lds_read<S>(&sm.b[wave][0][t][sg * S], bt);
-            lds_read<S>(&sm.b[wave][1][t][sg * S], ct);
+        for (int tq = 0; tq < L; tq += 4) {
+            float bq[NB][4];
 #pragma unroll
-            for (int s = 0; s < S; ++s) dc[s] = 0.f;
+            for (int i = 0; i < NB; ++i)
+                if constexpr (BY_STATE) lds_read<4>(&sm.bt[wave][n0 + 4 * i][tq], bq[i]);
 #pragma unroll
-            for (int c = 0; c < C; ++c) {
-                sv[t][c] = 0.f;
+            for (int k = 0; k < 4; ++k) {
+                const int t = tq + k;
+                __builtin_amdgcn_sched_barrier(0);
+                float x[2 * C], gs[C], ct[S], bt[NB], bw[S], dc[S];
+                lds_read<2 * C>(sm.x[wave][t][cl], x);
+                lds_read<C>(sm.ds[wave][t][cl], gs);
+                if constexpr (GATED) lds_read<S>(&sm.c[wave][t][sg * S], ct);
 #pragma unroll
-                for (int s = 0; s < S; ++s) {
-                    ah[t][s][c] = a[t][s][c] * hv[c * S + s];
-                    hv[c * S + s] = fmaf(x[C + c], bt[s], ah[t][s][c]);
-                    sv[t][c] = fmaf(ct[s], hv[c * S + s], sv[t][c]);
-                    dc[s] = fmaf(gs[c], hv[c * S + s], dc[s]);
+                for (int i = 0; i < NB; ++i)
+                    if constexpr (BY_STATE) bt[i] = bq[i][k];
+                if constexpr (!BY_STATE) lds_read<S>(&sm.b[wave][t][sg * S], bw);
+#pragma unroll
+                for (int c = 0; c < C; ++c) sv[k][c] = 0.f;
+                for_each<S>([&](auto si) {
+                    constexpr int s = decltype(si)::value;
+                    float bs;
+                    if constexpr (BY_STATE) bs = QR::template get<s>(bt);
+                    else bs = bw[s];
+#pragma unroll
+                    for (int c = 0; c < C; ++c) {
+                        float &h = hv[c * S + s];
+                        ah[t][s][c] = a[t][s][c] * h;
+                        h = fmaf(a[t][s][c], h, bs * x[C + c]);
+                        if constexpr (GATED) sv[k][c] = fmaf(ct[s], h, sv[k][c]);
+                        dc[s] = c == 0 ? gs[c] * h : fmaf(gs[c], h, dc[s]);
+                    }
+                });
+                if constexpr (GATED) pin(sv[k]);
+#pragma unroll
+                for (int s = 0; s < S; ++s) sm.red[wave][cl][sg * V + t % TR * S + s] = dc[s];
+                if (t % TR == TR - 1) {
+                    wave_lds_sync();
+                    join_channels<S, TR>(sm.red[wave], lane, [&](int tr, int n, float v) {
+                        const int tl = t - (TR - 1) + tr;
+                        if (tl < rows && n < p.N) part_c[(t0 + tl) * brow + n] = v;
+                    });
+                    wave_lds_sync();
                 }
             }
-#pragma unroll
-            for (int s = 0; s < S; ++s) sm.red[wave][cl][sg * V + t % TR * S + s] = dc[s];
-            if (t % TR == TR - 1) {
-                wave_lds_fence();
-                join_channels<S, TR>(sm.red[wave], lane, [&](int tr, int n, float v) {
-                    const int64_t tt = t0 + t - (TR - 1) + tr;
-                    if (tt < p.T && n < p.N) part_c[tt * brow + n] = tt < len ? v : 0.f;
-                });
-                wave_lds_fence();
-            }
+            if constexpr (GATED) sg_join4(sv[0], sv[1], sv[2], sv[3], so[tq / 4]);
         }
         // g in reverse and everything that depends on it
-        float dxv[L][C], dd2[L][C];
+        LV::read(sm.r[wave], lane, gv);
+        float dxv[4][C], dd2[4][C];
 #pragma unroll
         for (int t = L - 1; t >= 0; --t) {
-            float x[2 * C], gs[C], bt[S], ct[S], db[S];
             __builtin_amdgcn_sched_barrier(0);
+            float x[2 * C], gs[C], bt[S], ct[S], db[S];
             lds_read<2 * C>(sm.x[wave][t][cl], x);
             lds_read<C>(sm.ds[wave][t][cl], gs);
-            lds_read<S>(&sm.b[wave][0][t][sg * S], bt);
-            lds_read<S>(&sm.b[wave][1][t][sg * S], ct);
-#pragma unroll
-            for (int s = 0; s < S; ++s) db[s] = 0.f;
+            lds_read<S>(&sm.b[wave][t][sg * S], bt);
+            lds_read<S>(&sm.c[wave][t][sg * S], ct);
+            float (&dx)[C] = dxv[t % 4], (&dd)[C] = dd2[t % 4];
 #pragma unroll
             for (int c = 0; c < C; ++c) {
-                dxv[t][c] = dd2[t][c] = 0.f;
+                dx[c] = dd[c] = 0.f;
 #pragma unroll
                 for (int s = 0; s < S; ++s) {
                     const float gt = fmaf(ct[s], gs[c], gv[c * S + s]);
                     gv[c * S + s] = a[t][s][c] * gt;
                     const float q = gt * ah[t][s][c];
-                    dxv[t][c] = fmaf(gt, bt[s], dxv[t][c]);
-                    db[s] = fmaf(gt, x[C + c], db[s]);
-                    dd2[t][c] = fmaf(q, A2[s][c], dd2[t][c]);
+                    dx[c] = fmaf(gt, bt[s], dx[c]);
+                    db[s] = c == 0 ? gt * x[C + c] : fmaf(gt, x[C + c], db[s]);
+                    dd[c] = fmaf(q, A2[s][c], dd[c]);
                     dA[s][c] = fmaf(q, x[c], dA[s][c]);
                 }
             }
+            pin(dx);
+            pin(dd);
+#pragma unroll
+            for (int s = 0; s < S; ++s) pin(dA[s]);
 #pragma unroll
             for (int s = 0; s < S; ++s) sm.red[wave][cl][sg * V + t % TR * S + s] = db[s];
             if (t % TR == 0) {
-                wave_lds_fence();
+                wave_lds_sync();
                 join_channels<S, TR>(sm.red[wave], lane, [&](int tr, int n, float v) {
-                    const int64_t tt = t0 + t + tr;
-                    if (tt < p.T && n < p.N) part_b[tt * brow + n] = tt < len ? v : 0.f;
+                    const int tl = t + tr;
+                    if (tl < rows && n < p.N) part_b[(t0 + tl) * brow + n] = v;
                 });
-                wave_lds_fence();
+                wave_lds_sync();
             }
-        }
-        float so[J][C], xo[J][C], ao[J][C];
-        if (z) sg_join<L, C>(sv, so);
-        sg_join<L, C>(dxv, xo);
-        sg_join<L, C>(dd2, ao);
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-            const int64_t t = t0 + 4 * j + sg;
-            if (t < p.T) {
-                const bool in = t < len;
-                float o1[C], o2[C], o3[C];
+            if (t % 4 == 0) {  // four steps are complete: their rows
+                const int j = t / 4;
+                float xo[C], ao[C], o1[C], o2[C], o3[C], uu[C], zz[C], gy[C], xr[2 * C], dsr[C];
+                sg_join4(dxv[0], dxv[1], dxv[2], dxv[3], xo);
+                sg_join4(dd2[0], dd2[1], dd2[2], dd2[3], ao);
+                PC::unpack(uk[j], uu);
+                PC::unpack(gk[j], gy);
+                if constexpr (GATED) PC::unpack(zk[j], zz);
+                lds_read<2 * C>(sm.x[wave][t + sg][cl], xr);
+                lds_read<C>(sm.ds[wave][t + sg][cl], dsr);
+                const bool in = t + sg < left;
 #pragma unroll
                 for (int c = 0; c < C; ++c) {
-                    const float dx = xo[j][c];
-                    o1[c] = in ? fmaf(dl[j][c], dx, skip[c] * ds[j][c]) : 0.f;
-                    o2[c] = in ? fmaf(uu[j][c], dx, LN2 * ao[j][c]) * der[j][c] : 0.f;
-                    if (in && c < nv) {
-                        dskip[c] = fmaf(ds[j][c], uu[j][c], dskip[c]);
-                        dbias[c] += o2[c];
-                    }
-                    if (z) {
-                        const float sk = fmaf(skip[c], uu[j][c], so[j][c]);
-                        o3[c] = in ? gy[j][c] * sk * dsilu(zz[j][c], sigmoid(zz[j][c])) : 0.f;
-                    }
+                    o1[c] = in ? fmaf(xr[c], xo[c], skip[c] * dsr[c]) : 0.f;
+                    o2[c] = in ? fmaf(uu[c], xo[c], LN2 * ao[c]) * der[j][c] : 0.f;
+                    dskip[c] = fmaf(dsr[c], uu[c], dskip[c]);
+                    dbias[c] += o2[c];
+                    if constexpr (GATED)
+                        o3[c] = in ? gy[c] * fmaf(skip[c], uu[c], so[j][c]) * dsilu(zz[c], sigmoid(zz[c])) : 0.f;
                 }
-                store_ch<T, C>(du + t * p.D, nv, vec, o1);
-                store_ch<T, C>(ddelta + t * p.D, nv, vec, o2);
-                if (z) store_ch<T, C>(dz + t * p.D, nv, vec, o3);
+                if (t + sg < rows) {
+                    const int64_t at = row0 + t0 * p.D;
+                    store_ch<T, C>(reinterpret_cast<char *>(static_cast<T *>(p.du) + at) + voff[j], nv, whole, o1);
+                    store_ch<T, C>(reinterpret_cast<char *>(static_cast<T *>(p.ddelta) + at) + voff[j], nv, whole, o2);
+                    if constexpr (GATED)
+                        store_ch<T, C>(reinterpret_cast<char *>(static_cast<T *>(p.dz) + at) + voff[j], nv, whole, o3);
+                }
             }
         }
     }
 #pragma unroll
     for (int f = 0; f < FPT; ++f)
-        if (st_off[f] >= 0 && p.dh0) p.dh0[b * p.D * p.N + st_off[f]] = carry[f];
+        if (st_off[f] >= 0 && p.dh0) p.dh0[st_base + st_off[f]] = carry[f];
     // dA over the waves; dskip and ddelta_bias over the waves and lane rows too
-    __syncthreads();
+    wg_lds_sync();
     float ev[EL];
 #pragma unroll
     for (int c = 0; c < C; ++c)
@@ -338,7 +414,7 @@ __global__ __launch_bounds__(NW * 64) void scan_bwd_kernel(ScanArgs p) {
         sm.red[wave][cl][sg * 2 * C + c] = dskip[c];
         sm.red[wave][cl][sg * 2 * C + C + c] = dbias[c];
     }
-    __syncthreads();
+    wg_lds_sync();
     float *pa = p.part_a + b * (p.N + 2) * p.D;
 #pragma unroll
     for (int f = 0; f < FPT; ++f) {
@@ -347,8 +423,8 @@ __global__ __launch_bounds__(NW * 64) void scan_bwd_kernel(ScanArgs p) {
             float s = 0.f;
 #pragma unroll
             for (int w = 0; w < NW; ++w) s += sm.s[w][i];
-            const int64_t d = st_off[f] / p.N, n = st_off[f] - d * p.N;
-            pa[n * p.D + d] = s;
+            const int ch = st_off[f] / (int)p.N, n = st_off[f] - ch * (int)p.N;
+            pa[n * p.D + d0 + ch] = s;
         }
     }
     if (tid < 16 * 2 * C) {
@@ -403,7 +479,8 @@ mi_status launch_bwd(ScanArgs a, hipStream_t s) {
     int64_t items;
     if (!mul_ok(a.B, a.G, a.tiles, 1, &items) || items > 0x7ffffff0) return MI_ERR_UNSUPPORTED;
     a.n_items = (int)items;
-    const auto kernel = scan_bwd_kernel<T, S, TL::C, TL::L, SCAN_NW>;
+    const auto kernel = a.z ? scan_bwd_kernel<T, S, TL::C, TL::L, SCAN_NW, true>
+                            : scan_bwd_kernel<T, S, TL::C, TL::L, SCAN_NW, false>;
     if (hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
                             (int)sizeof(SH)) != hipSuccess)
         return MI_ERR_LAUNCH;
@@ -478,7 +555,7 @@ mi_status mi_selective_scan_bwd(const void *u, const void *delta, const float *A
     a.lengths = lengths; a.states = const_cast<float *>(states); a.dy = dy; a.dhT = dhT; a.du = du;
     a.ddelta = ddelta; a.dz = dz; a.dh0 = dh0;
     a.B = B; a.T = T; a.D = D; a.N = N; a.softplus = softplus_on != 0;
-    if (D / G > 0x40000000 || G > 0x40000000) return MI_ERR_UNSUPPORTED;
+    if (D > SCAN_MAX_D || G * N > SCAN_MAX_D) return MI_ERR_UNSUPPORTED;
     a.G = (int)G; a.per = (int)(D / G);
     a.vec = scan_vec(a, dt);
     if (B > 0) {
