@@ -312,7 +312,7 @@ mi_status launch_tile(ScanArgs a, hipStream_t s) {
 //    (249 and 237).
 template <typename T, int S>
 mi_status launch_fwd(const ScanArgs &a, hipStream_t s) {
-    constexpr int C = ScanTile<S>::C, L = ScanTile<S>::L;
+    constexpr int C = FwdTile<S>::C, L = FwdTile<S>::L;
     constexpr int LN = S >= 8 ? 4 : S >= 2 ? 8 : 16;  // at most 32 gates a lane: 128 registers (64 gates for S = 16)
     const int64_t n = a.B * a.G * ((a.per + 16 * C - 1) / (16 * C));
     if (n >= 768) return launch_tile<T, S, C, L, 4, S == 2 || S == 16 ? 2 : 3>(a, s);

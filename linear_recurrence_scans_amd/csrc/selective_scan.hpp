@@ -41,36 +41,38 @@ struct ScanArgs {
     int vec;               // rows may be read C channels at a time
 };
 
-// Tile constants of a state count: S states a lane; C channels a lane and L
-// steps a wave follow from a budget of 64 gates a lane (128 vector registers
-// for gates and products in the backward).
-template <int S> struct ScanTile;
-template <> struct ScanTile<1> { static constexpr int C = 2, L = 16; };
-template <> struct ScanTile<2> { static constexpr int C = 2, L = 16; };
-template <> struct ScanTile<4> { static constexpr int C = 2, L = 8; };
-template <> struct ScanTile<8> { static constexpr int C = 1, L = 8; };
-template <> struct ScanTile<16> { static constexpr int C = 1, L = 4; };
+// Tiles by S, the states a lane holds: C channels a lane, L steps a wave, NW waves
+// a workgroup.  S C L is the gates a lane keeps: 64, or 32 for S = 1 and 2, whose
+// rows fill the LDS first.  A block of the backward, NW L steps, is also the
+// distance of the states that the forward saves for it.  (The backward with 32
+// gates and 16 waves a workgroup, four a SIMD, is slower at N = 16: 630 us against
+// 535 for B = 4, T = 4096, D = 2048; its folds are twice as many and twice as long.)
+template <int S> struct FwdTile;
+template <> struct FwdTile<1> { static constexpr int C = 2, L = 16; };
+template <> struct FwdTile<2> { static constexpr int C = 2, L = 8; };
+template <> struct FwdTile<4> { static constexpr int C = 2, L = 8; };
+template <> struct FwdTile<8> { static constexpr int C = 1, L = 8; };
+template <> struct FwdTile<16> { static constexpr int C = 1, L = 4; };
+template <int S> struct BwdTile : FwdTile<S> { static constexpr int NW = 8; };
 
-constexpr int SCAN_NW = 8;  // waves a workgroup
 // Rows inside a block are addressed with 32-bit byte offsets: 16 rows of D
 // (or G N) 4-byte values stay below 2^31.
 constexpr int64_t SCAN_MAX_D = 1 << 24;
 
 inline int scan_s(int64_t N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }
 
-// Steps between two saved states: a block of the backward.
+// Steps between two saved states.
+template <int S>
+__host__ __device__ constexpr int64_t scan_block_of() { return BwdTile<S>::NW * BwdTile<S>::L; }
 inline int64_t scan_block(int64_t N) {
     switch (scan_s(N)) {
-        case 1: return SCAN_NW * ScanTile<1>::L;
-        case 2: return SCAN_NW * ScanTile<2>::L;
-        case 4: return SCAN_NW * ScanTile<4>::L;
-        case 8: return SCAN_NW * ScanTile<8>::L;
+        case 1: return scan_block_of<1>();
+        case 2: return scan_block_of<2>();
+        case 4: return scan_block_of<4>();
+        case 8: return scan_block_of<8>();
     }
-    return SCAN_NW * ScanTile<16>::L;
+    return scan_block_of<16>();
 }
-
-template <int S>
-__host__ __device__ constexpr int64_t scan_block_of() { return SCAN_NW * ScanTile<S>::L; }
 
 struct ScanSizes {
     int64_t x, bc, h, a, d, states;  // bytes of (B,T,D), Bm, (B,D,N), A, (D), states
@@ -241,6 +243,20 @@ __device__ __forceinline__ void lds_read(const float *p, float (&f)[N]) {
     } else {
 #pragma unroll
         for (int i = 0; i < N; ++i) f[i] = p[i];
+    }
+}
+
+// N consecutive floats of a lane's own.
+template <int N>
+__device__ __forceinline__ void lds_write(float *p, const float (&f)[N]) {
+    if constexpr (N % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) *reinterpret_cast<f32x4 *>(p + i) = f32x4{f[i], f[i + 1], f[i + 2], f[i + 3]};
+    } else if constexpr (N == 2) {
+        *reinterpret_cast<f32x2 *>(p) = f32x2{f[0], f[1]};
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) p[i] = f[i];
     }
 }
 

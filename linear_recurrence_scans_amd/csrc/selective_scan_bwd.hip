@@ -10,27 +10,53 @@
 // dBm and dCm sum over the channels of a group: C of them in the lane, sixteen
 // lanes through LDS, the tiles of a group through partial rows that
 // reduce_parts adds in a fixed order.
+#include <stddef.h>
+
 #include "checks.hpp"
 #include "selective_scan.hpp"
 
 namespace miscan {
 namespace {
 
-// Steps joined over the channel lanes at once: 32 values a lane, 16 for S = 16
-// (LDS).
-constexpr int join_steps(int S, int L) { return S == 16 ? 1 : 32 / S < L ? 32 / S : L; }
+// Steps joined over the channel lanes at once: 16 values a lane, so that the join
+// leaves one sum to every lane.
+constexpr int join_steps(int S, int L) { return 16 / S < L ? 16 / S : L; }
 
-template <int S, int C, int L, int NW>
-struct BwdShared {
+// LDS of a wave.  `join` holds the values to sum over the channel lanes (rows four
+// banks apart); it takes the place of s and p, which are done with by then.
+template <int S, int C, int L>
+struct BwdWave {
     static constexpr int E = S * C * 64, TR = join_steps(S, L), V = TR * S, ROW = 4 * V + 4;
-    float x[NW][L][16][2 * C];   // dl, dl u
-    float ds[NW][L][16][C];
-    static constexpr bool BY_STATE = S < 16;  // room for both orders of Bm
-    float bt[NW][BY_STATE ? 4 * S : 1][L + 4];  // Bm by state
-    float b[NW][L][4 * S];       // Bm by step
-    float c[NW][L][4 * S];       // Cm by step
-    float s[NW][E], p[NW][E], r[NW][E];
-    float red[NW][16][ROW];      // values to sum over the channel lanes; rows four banks apart
+    float x[L][16][2 * C];       // dl, dl u
+    float ds[L][16][C];
+    float b[L][4 * S];           // Bm
+    float c[L][4 * S];           // Cm
+    union {
+        struct { float s[E], p[E]; };
+        float join[16][ROW];
+    };
+    float r[E];
+    float keep[3][64][L / 4 * C];  // a lane's own u, softplus', dy silu'(z) from staging to the last rows
+};
+
+// One float of every wave's LDS.  An LDS access reaches 64 KiB past its address
+// register, less than the waves' span, so a register serves a few waves; the
+// asm keeps the compiler from a register for each.
+template <class W, int NW>
+struct WaveColumn {
+    static constexpr int REACH = 65536 / (int)sizeof(W);
+    float *base[(NW + REACH - 1) / REACH];
+    __device__ __forceinline__ WaveColumn(char *smem, int off) {
+#pragma unroll
+        for (int g = 0; g < (NW + REACH - 1) / REACH; ++g) {
+            int o = off + g * REACH * (int)sizeof(W);
+            asm volatile("" : "+v"(o));
+            base[g] = reinterpret_cast<float *>(smem + o);
+        }
+    }
+    __device__ __forceinline__ float &operator[](int w) const {
+        return base[w / REACH][w % REACH * (int)(sizeof(W) / 4)];
+    }
 };
 
 // Sums the sixteen channel lanes' values of TR steps and stores them: linear
@@ -55,22 +81,24 @@ __device__ __forceinline__ void join_channels(const float (*red)[ROW], int lane,
 template <typename T, int S, int C, int L, int NW, bool GATED>
 __global__ __launch_bounds__(NW * 64, 2) void scan_bwd_kernel(ScanArgs p) {
     constexpr int EL = S * C, J = L / 4, NP = 4 * S;
-    constexpr int E = EL * 64, NT = NW * 64, FPT = (E + NT - 1) / NT, BPL = (L * NP + 63) / 64;
+    constexpr int E = EL * 64, NT = NW * 64, BPL = (L * NP + 63) / 64;
+    constexpr int FPT = (2 * E + NT - 1) / NT;  // folds a thread: E forward, E in reverse
     using LV = LaneVec<EL>;
-    using QR = QuadRow<S>;
-    constexpr int NB = QR::NB;
     using PC = Pack<T, C>;
     using raw_t = typename PC::raw_t;
     using one_t = typename Pack<T, 1>::raw_t;
-    using SH = BwdShared<S, C, L, NW>;
-    constexpr int TR = SH::TR, V = SH::V;
-    constexpr bool BY_STATE = SH::BY_STATE;
+    using W = BwdWave<S, C, L>;
+    constexpr int TR = W::TR, V = W::V;
+    // Gates and products a_t h_{t-1} both stay in registers, up to 128 of them;
+    // with 16 states a lane the gates are formed again (3 of 28 issue slots).
+    constexpr bool KEEP = S < 16;
     extern __shared__ __align__(16) char smem[];
-    SH &sm = *reinterpret_cast<SH *>(smem);
+    W *const sm = reinterpret_cast<W *>(smem);
     const int item = xcd_item(p.n_items);
     if (item >= p.n_items) return;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    W &my = sm[wave];
     const int sg = lane >> 4, cl = lane & 15;
     const int tile = item % p.tiles;
     const int g = item / p.tiles % p.G;
@@ -96,17 +124,20 @@ __global__ __launch_bounds__(NW * 64, 2) void scan_bwd_kernel(ScanArgs p) {
             dA[s][c] = 0.f;
         }
     }
-    float carry[FPT], h0[FPT];  // gradient that enters the block from its right; state before the block
-    int st_off[FPT];            // offset from the tile's first state, or -1
+    // Folds: thread tid takes tasks tid, tid + NT, ...; task i < E folds the states
+    // of position i forward, task E + i the gradients in reverse.  `edge` is what
+    // enters the block: the saved state before it, the gradient from its right.
+    float edge[FPT];
+    int st_off[FPT];  // offset from the tile's first state, or -1
     const int64_t st_base = b * p.D * p.N + d0 * p.N;
 #pragma unroll
     for (int f = 0; f < FPT; ++f) {
         const int i = tid + f * NT;
         int ln, e;
-        LV::where(i < E ? i : 0, &ln, &e);
+        LV::where(i % E, &ln, &e);
         const int n = (ln >> 4) * S + e % S, ch = (ln & 15) * C + e / S;
-        st_off[f] = i < E && n < p.N && ch < nch ? ch * (int)p.N + n : -1;
-        carry[f] = st_off[f] >= 0 && p.dhT ? p.dhT[st_base + st_off[f]] : 0.f;
+        st_off[f] = i < 2 * E && n < p.N && ch < nch ? ch * (int)p.N + n : -1;
+        edge[f] = i >= E && st_off[f] >= 0 && p.dhT ? p.dhT[st_base + st_off[f]] : 0.f;
     }
     const uint32_t row = (uint32_t)(p.D * (int64_t)sizeof(T));
     uint32_t voff[J], boff[BPL];
@@ -124,7 +155,6 @@ __global__ __launch_bounds__(NW * 64, 2) void scan_bwd_kernel(ScanArgs p) {
     float *part_b = p.part_bc + (int64_t)tile * 2 * bc + b0;
     float *part_c = part_b + bc;
     const int64_t n_blk = (p.T + NW * L - 1) / (NW * L);
-    const int n0 = QR::first(lane);
     raw_t ur[J], dr[J], zr[J], gr[J];
     one_t br[BPL], cr[BPL];
 
@@ -147,50 +177,51 @@ __global__ __launch_bounds__(NW * 64, 2) void scan_bwd_kernel(ScanArgs p) {
         }
         const float *st = p.states + (b * n_blk + blk) * p.D * p.N + d0 * p.N;
 #pragma unroll
-        for (int f = 0; f < FPT; ++f) h0[f] = st_off[f] >= 0 ? st[st_off[f]] : 0.f;
+        for (int f = 0; f < FPT; ++f)
+            if (tid + f * NT < E) edge[f] = st_off[f] >= 0 ? st[st_off[f]] : 0.f;
     };
 
     if (n_blk > 0) load(n_blk - 1);
     for (int64_t blk = n_blk - 1; blk >= 0; --blk) {
         const int64_t t0 = blk * (NW * L) + wave * L;
         const int left = steps_left<L>(t0, len), rows = steps_left<L>(t0, p.T);
-        raw_t uk[J], zk[J], gk[J];
-        float der[J][C], hin[FPT];
+        {
+            float uu[J * C], der[J * C], gz[J * C];
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-            float uu[C], dd[C], zz[C], gy[C];
-            PC::unpack(ur[j], uu);
-            PC::unpack(dr[j], dd);
-            PC::unpack(gr[j], gy);
-            if constexpr (GATED) PC::unpack(zr[j], zz);
-            uk[j] = ur[j];
-            gk[j] = gr[j];
-            if constexpr (GATED) zk[j] = zr[j];
-            const bool in = 4 * j + sg < left;
+            for (int j = 0; j < J; ++j) {
+                float u[C], dd[C], z[C], gy[C], x[2 * C];
+                PC::unpack(ur[j], u);
+                PC::unpack(dr[j], dd);
+                PC::unpack(gr[j], gy);
+                if constexpr (GATED) PC::unpack(zr[j], z);
+                const bool in = 4 * j + sg < left;
 #pragma unroll
-            for (int c = 0; c < C; ++c) {
-                float r = gate_rate(dd[c] + bias[c], p.softplus, &der[j][c]);
-                r = in ? r : 0.f;
-                sm.x[wave][4 * j + sg][cl][c] = r;
-                sm.x[wave][4 * j + sg][cl][C + c] = r * uu[c];
-                if constexpr (GATED) gy[c] *= silu(zz[c]);
-                sm.ds[wave][4 * j + sg][cl][c] = gy[c];
+                for (int c = 0; c < C; ++c) {
+                    const float r = gate_rate(dd[c] + bias[c], p.softplus, &der[j * C + c]);
+                    x[c] = in ? r : 0.f;
+                    x[C + c] = x[c] * u[c];
+                    uu[j * C + c] = u[c];
+                    if constexpr (GATED) {
+                        const float sig = sigmoid(z[c]);
+                        gz[j * C + c] = gy[c] * dsilu(z[c], sig);
+                        gy[c] *= z[c] * sig;
+                    }
+                }
+                lds_write<2 * C>(my.x[4 * j + sg][cl], x);
+                lds_write<C>(my.ds[4 * j + sg][cl], gy);
             }
+            lds_write<J * C>(my.keep[0][lane], uu);
+            lds_write<J * C>(my.keep[1][lane], der);
+            if constexpr (GATED) lds_write<J * C>(my.keep[2][lane], gz);
         }
 #pragma unroll
         for (int i = 0; i < BPL; ++i) {
             const int q = lane + 64 * i, t = q / NP, n = q % NP;
             if (L * NP % 64 == 0 || q < L * NP) {
-                float f;
-                Pack<T, 1>::unpack(br[i], &f);
-                if constexpr (BY_STATE) sm.bt[wave][n][t] = f;
-                sm.b[wave][t][n] = f;
-                Pack<T, 1>::unpack(cr[i], &sm.c[wave][t][n]);
+                Pack<T, 1>::unpack(br[i], &my.b[t][n]);
+                Pack<T, 1>::unpack(cr[i], &my.c[t][n]);
             }
         }
-#pragma unroll
-        for (int f = 0; f < FPT; ++f) hin[f] = h0[f];
-        if (blk > 0) load(blk - 1);
         wave_lds_sync();
         // local scans, forward and reverse
         float a[L][S][C];
@@ -200,45 +231,30 @@ __global__ __launch_bounds__(NW * 64, 2) void scan_bwd_kernel(ScanArgs p) {
 #pragma unroll
             for (int c = 0; c < C; ++c) sum[c] = 0.f;
 #pragma unroll
-            for (int tq = 0; tq < L; tq += 4) {
-                float bq[NB][4];
+            for (int t = 0; t < L; ++t) {
+                __builtin_amdgcn_sched_barrier(0);
+                float x[2 * C], bt[S];
+                lds_read<2 * C>(my.x[t][cl], x);
+                lds_read<S>(&my.b[t][sg * S], bt);
 #pragma unroll
-                for (int i = 0; i < NB; ++i)
-                    if constexpr (BY_STATE) lds_read<4>(&sm.bt[wave][n0 + 4 * i][tq], bq[i]);
+                for (int c = 0; c < C; ++c) {
+                    sum[c] += x[c];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int t = tq + k;
-                    __builtin_amdgcn_sched_barrier(0);
-                    float x[2 * C], bt[NB], bw[S];
-                    lds_read<2 * C>(sm.x[wave][t][cl], x);
-#pragma unroll
-                    for (int i = 0; i < NB; ++i)
-                        if constexpr (BY_STATE) bt[i] = bq[i][k];
-                    if constexpr (!BY_STATE) lds_read<S>(&sm.b[wave][t][sg * S], bw);
-#pragma unroll
-                    for (int c = 0; c < C; ++c) sum[c] += x[c];
-                    for_each<S>([&](auto si) {
-                        constexpr int s = decltype(si)::value;
-                        float bs;
-                        if constexpr (BY_STATE) bs = QR::template get<s>(bt);
-                        else bs = bw[s];
-#pragma unroll
-                        for (int c = 0; c < C; ++c) {
-                            a[t][s][c] = __builtin_amdgcn_exp2f(x[c] * A2[s][c]);
-                            const float xb = bs * x[C + c];
-                            hv[c * S + s] = t == 0 ? xb : fmaf(a[t][s][c], hv[c * S + s], xb);
-                        }
-                    });
-                    pin(hv);
+                    for (int s = 0; s < S; ++s) {
+                        a[t][s][c] = __builtin_amdgcn_exp2f(x[c] * A2[s][c]);
+                        const float xb = bt[s] * x[C + c];
+                        hv[c * S + s] = t == 0 ? xb : fmaf(a[t][s][c], hv[c * S + s], xb);
+                    }
                 }
+                pin(hv);
             }
-            LV::write(sm.s[wave], lane, hv);
+            LV::write(my.s, lane, hv);
 #pragma unroll
             for (int t = L - 1; t >= 0; --t) {
                 __builtin_amdgcn_sched_barrier(0);
                 float gs[C], ct[S];
-                lds_read<C>(sm.ds[wave][t][cl], gs);
-                lds_read<S>(&sm.c[wave][t][sg * S], ct);
+                lds_read<C>(my.ds[t][cl], gs);
+                lds_read<S>(&my.c[t][sg * S], ct);
 #pragma unroll
                 for (int c = 0; c < C; ++c)
 #pragma unroll
@@ -247,98 +263,110 @@ __global__ __launch_bounds__(NW * 64, 2) void scan_bwd_kernel(ScanArgs p) {
                             a[t][s][c] * (t == L - 1 ? ct[s] * gs[c] : fmaf(ct[s], gs[c], gv[c * S + s]));
                 pin(gv);
             }
-            LV::write(sm.r[wave], lane, gv);
+            LV::write(my.r, lane, gv);
 #pragma unroll
             for (int c = 0; c < C; ++c)
 #pragma unroll
                 for (int s = 0; s < S; ++s) hv[c * S + s] = __builtin_amdgcn_exp2f(sum[c] * A2[s][c]);
-            LV::write(sm.p[wave], lane, hv);
+            LV::write(my.p, lane, hv);
         }
         wg_lds_sync();
 #pragma unroll
         for (int f = 0; f < FPT; ++f) {
-            const int i = tid + f * NT;
-            if (i < E) {
-                float h = hin[f], gc = carry[f], pw[NW], sv[NW], rv[NW];
+            const int task = tid + f * NT;
+            if (task < 2 * E) {
+                // forward: s and p of waves 0, 1, ...; reverse: r and p of waves NW - 1, ...
+                const bool rev = task >= E;
+                const int i = rev ? task - E : task;
+                WaveColumn<W, NW> val(smem, (int)(rev ? offsetof(W, r) : offsetof(W, s)) + i * 4);
+                const WaveColumn<W, NW> gate(smem, (int)offsetof(W, p) + i * 4);
+                float c = edge[f], pw[NW], v[NW];
 #pragma unroll
                 for (int w = 0; w < NW; ++w) {
-                    pw[w] = sm.p[w][i];
-                    sv[w] = sm.s[w][i];
-                    rv[w] = sm.r[w][i];
+                    pw[w] = gate[w];
+                    v[w] = val[w];
                 }
+                if (rev) {
 #pragma unroll
-                for (int w = 0; w < NW; ++w) {
-                    sm.s[w][i] = h;
-                    h = fmaf(pw[w], h, sv[w]);
-                    sm.r[NW - 1 - w][i] = gc;
-                    gc = fmaf(pw[NW - 1 - w], gc, rv[NW - 1 - w]);
+                    for (int w = NW - 1; w >= 0; --w) {
+                        val[w] = c;
+                        c = fmaf(pw[w], c, v[w]);
+                    }
+                    edge[f] = c;
+                } else {
+#pragma unroll
+                    for (int w = 0; w < NW; ++w) {
+                        val[w] = c;
+                        c = fmaf(pw[w], c, v[w]);
+                    }
                 }
-                carry[f] = gc;
             }
         }
         wg_lds_sync();
-        LV::read(sm.s[wave], lane, hv);
+        LV::read(my.s, lane, hv);
+        wave_lds_sync();
         // states: keep a_t h_{t-1}; s_t for the gate's gradient; dCm
-        float ah[L][S][C], sv[4][C], so[J][C];
+        float sv[4][C], ah[KEEP ? L : 1][S][C];
 #pragma unroll
         for (int tq = 0; tq < L; tq += 4) {
-            float bq[NB][4];
-#pragma unroll
-            for (int i = 0; i < NB; ++i)
-                if constexpr (BY_STATE) lds_read<4>(&sm.bt[wave][n0 + 4 * i][tq], bq[i]);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int t = tq + k;
                 __builtin_amdgcn_sched_barrier(0);
-                float x[2 * C], gs[C], ct[S], bt[NB], bw[S], dc[S];
-                lds_read<2 * C>(sm.x[wave][t][cl], x);
-                lds_read<C>(sm.ds[wave][t][cl], gs);
-                if constexpr (GATED) lds_read<S>(&sm.c[wave][t][sg * S], ct);
+                float x[2 * C], gs[C], bt[S], ct[S], dc[S];
+                lds_read<2 * C>(my.x[t][cl], x);
+                lds_read<C>(my.ds[t][cl], gs);
+                lds_read<S>(&my.b[t][sg * S], bt);
+                if constexpr (GATED) lds_read<S>(&my.c[t][sg * S], ct);
 #pragma unroll
-                for (int i = 0; i < NB; ++i)
-                    if constexpr (BY_STATE) bt[i] = bq[i][k];
-                if constexpr (!BY_STATE) lds_read<S>(&sm.b[wave][t][sg * S], bw);
+                for (int c = 0; c < C; ++c) {
+                    sv[k][c] = 0.f;
 #pragma unroll
-                for (int c = 0; c < C; ++c) sv[k][c] = 0.f;
-                for_each<S>([&](auto si) {
-                    constexpr int s = decltype(si)::value;
-                    float bs;
-                    if constexpr (BY_STATE) bs = QR::template get<s>(bt);
-                    else bs = bw[s];
-#pragma unroll
-                    for (int c = 0; c < C; ++c) {
+                    for (int s = 0; s < S; ++s) {
                         float &h = hv[c * S + s];
-                        ah[t][s][c] = a[t][s][c] * h;
-                        h = fmaf(a[t][s][c], h, bs * x[C + c]);
+                        const float p_h = a[t][s][c] * h;
+                        if constexpr (KEEP) ah[t][s][c] = p_h;
+                        else a[t][s][c] = p_h;
+                        h = fmaf(bt[s], x[C + c], p_h);
                         if constexpr (GATED) sv[k][c] = fmaf(ct[s], h, sv[k][c]);
                         dc[s] = c == 0 ? gs[c] * h : fmaf(gs[c], h, dc[s]);
                     }
-                });
+                }
+                pin(hv);
                 if constexpr (GATED) pin(sv[k]);
-#pragma unroll
-                for (int s = 0; s < S; ++s) sm.red[wave][cl][sg * V + t % TR * S + s] = dc[s];
+                lds_write<S>(&my.join[cl][sg * V + t % TR * S], dc);
                 if (t % TR == TR - 1) {
                     wave_lds_sync();
-                    join_channels<S, TR>(sm.red[wave], lane, [&](int tr, int n, float v) {
+                    join_channels<S, TR>(my.join, lane, [&](int tr, int n, float v) {
                         const int tl = t - (TR - 1) + tr;
                         if (tl < rows && n < p.N) part_c[(t0 + tl) * brow + n] = v;
                     });
                     wave_lds_sync();
                 }
             }
-            if constexpr (GATED) sg_join4(sv[0], sv[1], sv[2], sv[3], so[tq / 4]);
+            if constexpr (GATED) {  // four steps' s are complete: dz
+                float so[C], uu[C], gz[C], o[C];
+                sg_join4(sv[0], sv[1], sv[2], sv[3], so);
+                lds_read<C>(&my.keep[0][lane][tq / 4 * C], uu);
+                lds_read<C>(&my.keep[2][lane][tq / 4 * C], gz);
+#pragma unroll
+                for (int c = 0; c < C; ++c) o[c] = tq + sg < left ? gz[c] * fmaf(skip[c], uu[c], so[c]) : 0.f;
+                if (tq + sg < rows)
+                    store_ch<T, C>(reinterpret_cast<char *>(static_cast<T *>(p.dz) + row0 + t0 * p.D) + voff[tq / 4],
+                                   nv, whole, o);
+            }
         }
         // g in reverse and everything that depends on it
-        LV::read(sm.r[wave], lane, gv);
+        LV::read(my.r, lane, gv);
         float dxv[4][C], dd2[4][C];
-#pragma unroll
-        for (int t = L - 1; t >= 0; --t) {
+        for_each<L>([&](auto ri) {
+            constexpr int t = L - 1 - decltype(ri)::value;
             __builtin_amdgcn_sched_barrier(0);
             float x[2 * C], gs[C], bt[S], ct[S], db[S];
-            lds_read<2 * C>(sm.x[wave][t][cl], x);
-            lds_read<C>(sm.ds[wave][t][cl], gs);
-            lds_read<S>(&sm.b[wave][t][sg * S], bt);
-            lds_read<S>(&sm.c[wave][t][sg * S], ct);
+            lds_read<2 * C>(my.x[t][cl], x);
+            lds_read<C>(my.ds[t][cl], gs);
+            lds_read<S>(&my.b[t][sg * S], bt);
+            lds_read<S>(&my.c[t][sg * S], ct);
             float (&dx)[C] = dxv[t % 4], (&dd)[C] = dd2[t % 4];
 #pragma unroll
             for (int c = 0; c < C; ++c) {
@@ -346,8 +374,14 @@ __global__ __launch_bounds__(NW * 64, 2) void scan_bwd_kernel(ScanArgs p) {
 #pragma unroll
                 for (int s = 0; s < S; ++s) {
                     const float gt = fmaf(ct[s], gs[c], gv[c * S + s]);
-                    gv[c * S + s] = a[t][s][c] * gt;
-                    const float q = gt * ah[t][s][c];
+                    float q;
+                    if constexpr (KEEP) {
+                        gv[c * S + s] = a[t][s][c] * gt;
+                        q = gt * ah[t][s][c];
+                    } else {
+                        gv[c * S + s] = t > 0 ? __builtin_amdgcn_exp2f(x[c] * A2[s][c]) * gt : 0.f;
+                        q = gt * a[t][s][c];
+                    }
                     dx[c] = fmaf(gt, bt[s], dx[c]);
                     db[s] = c == 0 ? gt * x[C + c] : fmaf(gt, x[C + c], db[s]);
                     dd[c] = fmaf(q, A2[s][c], dd[c]);
@@ -358,71 +392,66 @@ __global__ __launch_bounds__(NW * 64, 2) void scan_bwd_kernel(ScanArgs p) {
             pin(dd);
 #pragma unroll
             for (int s = 0; s < S; ++s) pin(dA[s]);
-#pragma unroll
-            for (int s = 0; s < S; ++s) sm.red[wave][cl][sg * V + t % TR * S + s] = db[s];
-            if (t % TR == 0) {
+            lds_write<S>(&my.join[cl][sg * V + t % TR * S], db);
+            if constexpr (t % TR == 0) {
                 wave_lds_sync();
-                join_channels<S, TR>(sm.red[wave], lane, [&](int tr, int n, float v) {
+                join_channels<S, TR>(my.join, lane, [&](int tr, int n, float v) {
                     const int tl = t + tr;
                     if (tl < rows && n < p.N) part_b[(t0 + tl) * brow + n] = v;
                 });
                 wave_lds_sync();
             }
-            if (t % 4 == 0) {  // four steps are complete: their rows
-                const int j = t / 4;
-                float xo[C], ao[C], o1[C], o2[C], o3[C], uu[C], zz[C], gy[C], xr[2 * C], dsr[C];
+            if constexpr (t == L / 2) {  // half the gates are done with: registers for the next block's rows
+                if (blk > 0) load(blk - 1);
+            }
+            if constexpr (t % 4 == 0) {  // four steps are complete: their rows
+                constexpr int j = t / 4;
+                float xo[C], ao[C], o1[C], o2[C], uu[C], der[C], xr[2 * C], dsr[C];
                 sg_join4(dxv[0], dxv[1], dxv[2], dxv[3], xo);
                 sg_join4(dd2[0], dd2[1], dd2[2], dd2[3], ao);
-                PC::unpack(uk[j], uu);
-                PC::unpack(gk[j], gy);
-                if constexpr (GATED) PC::unpack(zk[j], zz);
-                lds_read<2 * C>(sm.x[wave][t + sg][cl], xr);
-                lds_read<C>(sm.ds[wave][t + sg][cl], dsr);
+                lds_read<C>(&my.keep[0][lane][j * C], uu);
+                lds_read<C>(&my.keep[1][lane][j * C], der);
+                lds_read<2 * C>(my.x[t + sg][cl], xr);
+                lds_read<C>(my.ds[t + sg][cl], dsr);
                 const bool in = t + sg < left;
 #pragma unroll
                 for (int c = 0; c < C; ++c) {
                     o1[c] = in ? fmaf(xr[c], xo[c], skip[c] * dsr[c]) : 0.f;
-                    o2[c] = in ? fmaf(uu[c], xo[c], LN2 * ao[c]) * der[j][c] : 0.f;
+                    o2[c] = in ? fmaf(uu[c], xo[c], LN2 * ao[c]) * der[c] : 0.f;
                     dskip[c] = fmaf(dsr[c], uu[c], dskip[c]);
                     dbias[c] += o2[c];
-                    if constexpr (GATED)
-                        o3[c] = in ? gy[c] * fmaf(skip[c], uu[c], so[j][c]) * dsilu(zz[c], sigmoid(zz[c])) : 0.f;
                 }
                 if (t + sg < rows) {
                     const int64_t at = row0 + t0 * p.D;
                     store_ch<T, C>(reinterpret_cast<char *>(static_cast<T *>(p.du) + at) + voff[j], nv, whole, o1);
                     store_ch<T, C>(reinterpret_cast<char *>(static_cast<T *>(p.ddelta) + at) + voff[j], nv, whole, o2);
-                    if constexpr (GATED)
-                        store_ch<T, C>(reinterpret_cast<char *>(static_cast<T *>(p.dz) + at) + voff[j], nv, whole, o3);
                 }
             }
-        }
+        });
     }
 #pragma unroll
     for (int f = 0; f < FPT; ++f)
-        if (st_off[f] >= 0 && p.dh0) p.dh0[st_base + st_off[f]] = carry[f];
+        if (tid + f * NT >= E && st_off[f] >= 0 && p.dh0) p.dh0[st_base + st_off[f]] = edge[f];
     // dA over the waves; dskip and ddelta_bias over the waves and lane rows too
-    wg_lds_sync();
-    float ev[EL];
-#pragma unroll
-    for (int c = 0; c < C; ++c)
-#pragma unroll
-        for (int s = 0; s < S; ++s) ev[c * S + s] = dA[s][c];
-    LV::write(sm.s[wave], lane, ev);
+    float ev[EL], kb[2 * C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-        sm.red[wave][cl][sg * 2 * C + c] = dskip[c];
-        sm.red[wave][cl][sg * 2 * C + C + c] = dbias[c];
+        kb[c] = dskip[c];
+        kb[C + c] = dbias[c];
+#pragma unroll
+        for (int s = 0; s < S; ++s) ev[c * S + s] = dA[s][c];
     }
+    LV::write(my.r, lane, ev);
+    lds_write<2 * C>(my.x[sg][cl], kb);
     wg_lds_sync();
     float *pa = p.part_a + b * (p.N + 2) * p.D;
 #pragma unroll
     for (int f = 0; f < FPT; ++f) {
         const int i = tid + f * NT;
-        if (st_off[f] >= 0) {
+        if (i < E && st_off[f] >= 0) {
             float s = 0.f;
 #pragma unroll
-            for (int w = 0; w < NW; ++w) s += sm.s[w][i];
+            for (int w = 0; w < NW; ++w) s += sm[w].r[i];
             const int ch = st_off[f] / (int)p.N, n = st_off[f] - ch * (int)p.N;
             pa[n * p.D + d0 + ch] = s;
         }
@@ -434,7 +463,7 @@ __global__ __launch_bounds__(NW * 64, 2) void scan_bwd_kernel(ScanArgs p) {
 #pragma unroll
             for (int w = 0; w < NW; ++w)
 #pragma unroll
-                for (int q = 0; q < 4; ++q) s += sm.red[w][l][q * 2 * C + k];
+                for (int q = 0; q < 4; ++q) s += sm[w].x[q][l][k];
             pa[(p.N + k / C) * p.D + d0 + l * C + c] = s;
         }
     }
@@ -472,19 +501,19 @@ int64_t bwd_tiles(int64_t per, int64_t N) {
 
 template <typename T, int S>
 mi_status launch_bwd(ScanArgs a, hipStream_t s) {
-    using TL = ScanTile<S>;
-    using SH = BwdShared<S, TL::C, TL::L, SCAN_NW>;
-    static_assert(sizeof(SH) <= 160 * 1024, "a workgroup's LDS");
+    using TL = BwdTile<S>;
+    constexpr int SH = TL::NW * (int)sizeof(BwdWave<S, TL::C, TL::L>);
+    static_assert(SH <= 160 * 1024, "a workgroup's LDS");
     a.tiles = (int)bwd_tiles(a.per, a.N);
     int64_t items;
     if (!mul_ok(a.B, a.G, a.tiles, 1, &items) || items > 0x7ffffff0) return MI_ERR_UNSUPPORTED;
     a.n_items = (int)items;
-    const auto kernel = a.z ? scan_bwd_kernel<T, S, TL::C, TL::L, SCAN_NW, true>
-                            : scan_bwd_kernel<T, S, TL::C, TL::L, SCAN_NW, false>;
+    const auto kernel = a.z ? scan_bwd_kernel<T, S, TL::C, TL::L, TL::NW, true>
+                            : scan_bwd_kernel<T, S, TL::C, TL::L, TL::NW, false>;
     if (hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
-                            (int)sizeof(SH)) != hipSuccess)
+                            SH) != hipSuccess)
         return MI_ERR_LAUNCH;
-    hipLaunchKernelGGL(kernel, dim3(xcd_grid(a.n_items)), dim3(SCAN_NW * 64), sizeof(SH), s, a);
+    hipLaunchKernelGGL(kernel, dim3(xcd_grid(a.n_items)), dim3(TL::NW * 64), SH, s, a);
     return launch_status();
 }
 template <typename T>
