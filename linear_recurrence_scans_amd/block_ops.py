@@ -13,7 +13,7 @@ from __future__ import annotations
 
 import torch
 
-from . import _Call, _check, _dev_tensor, _device, _dt, _load, _nbytes, _out, _ptr, _same, _workspace
+from . import _Call, _check, _device, _dt, _load, _workspace
 
 __all__ = [
     "mi_causal_conv_fwd", "mi_causal_conv_bwd", "mi_causal_conv_bwd_workspace", "mi_causal_conv_step",
@@ -23,42 +23,87 @@ __all__ = [
 ]
 
 _ACTS = {None: 0, "silu": 1}
+_F32, _I32 = torch.float32, torch.int32
+
+
+# A step of a few microseconds on the GPU is bound by what the host does to
+# launch it, so the common call (torch's current stream and device) goes
+# without the context managers of a side stream.
+class _Here:
+    """Call on the current stream of the current device."""
+
+    __slots__ = ("handle",)
+
+    def __init__(self, handle):
+        self.handle = handle
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        return False
+
+    def keep(self, *ts):
+        pass
+
+
+# (tensors on a GPU have initialised torch's runtime, so the raw lookups are safe)
+_current_device = torch._C._cuda_getDevice
+_current_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _call(stream, device):
+    index = device.index
+    if stream is None and index == _current_device():
+        return _Here(_current_raw_stream(index))
+    return _Call(stream, device)
 
 
 def _act(act) -> int:
     try:
         return _ACTS[act]
-    except KeyError:
+    except (KeyError, TypeError):
         raise ValueError("act must be None or 'silu', not %r" % (act,)) from None
 
 
-def _opt(t, like: torch.Tensor, shape, name: str, dtype=None):
-    """Optional input of the given shape on `like`'s device (dtype: `like`'s by default)."""
-    if t is None:
-        return None
-    return _need(t, like, shape, name, dtype)
+def _dev_tensor(t, name: str) -> torch.Tensor:
+    _device(t, name)
+    return t if t.is_contiguous() else t.contiguous()
 
 
 def _need(t, like: torch.Tensor, shape, name: str, dtype=None):
-    t = _dev_tensor(t, name)
-    dtype = dtype or like.dtype
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != like.device:
-        raise ValueError("%s must be a %s tensor of shape %s on %s" % (name, dtype, tuple(shape), like.device))
-    return t
+    """An input of the given shape on `like`'s device (dtype: `like`'s by default)."""
+    _device(t, name)
+    if t.shape != shape or t.dtype != (dtype or like.dtype) or t.device != like.device:
+        raise ValueError("%s must be a %s tensor of shape %s on %s"
+                         % (name, dtype or like.dtype, tuple(shape), like.device))
+    return t if t.is_contiguous() else t.contiguous()
+
+
+def _opt(t, like: torch.Tensor, shape, name: str, dtype=None):
+    return None if t is None else _need(t, like, shape, name, dtype)
 
 
 def _new(t, like: torch.Tensor, shape, name: str, dtype=None):
     """An output: the caller's `t`, checked, or a new tensor."""
-    dtype = dtype or like.dtype
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != like.device or not t.is_contiguous():
+        return torch.empty(shape, dtype=dtype or like.dtype, device=like.device)
+    if t.shape != shape or t.dtype != (dtype or like.dtype) or t.device != like.device or not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s tensor of shape %s on %s"
-                         % (name, dtype, tuple(shape), like.device))
+                         % (name, dtype or like.dtype, tuple(shape), like.device))
     return t
 
 
-_F32, _I32 = torch.float32, torch.int32
+def _out(t, like: torch.Tensor, name: str):
+    return torch.empty_like(like) if t is None else _new(t, like, like.shape, name)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _nbytes(t) -> int:
+    return t.numel() * t.element_size()
 
 
 # ---------------------------------------------------------------------------
@@ -78,7 +123,7 @@ def mi_causal_conv_fwd(x, w, bias=None, x0=None, *, act=None, lengths=None, y=No
     bias (D), through `act` (None or "silu").  x0 (B, K-1, D) holds the inputs
     before the first step (None = zeros); xT (B, K-1, D) is the x0 of the
     sequence's continuation."""
-    with _Call(stream, _device(x, "x")) as c:
+    with _call(stream, _device(x, "x")) as c:
         x, w = _dev_tensor(x, "x"), _dev_tensor(w, "w")
         K = _conv_shape(x, w, 3)
         Bn, T, D = x.shape
@@ -102,7 +147,7 @@ def mi_causal_conv_bwd(x, w, bias, x0, dy, dxT=None, *, act=None, lengths=None, 
                        dx0=None, ws=None, stream=None):
     """(dx, dw, dbias, dx0): gradient of mi_causal_conv_fwd for dy (B, T, D) and,
     optionally, dxT (B, K-1, D); dbias and dx0 are None without bias and x0."""
-    with _Call(stream, _device(x, "x")) as c:
+    with _call(stream, _device(x, "x")) as c:
         x, w, dy = _dev_tensor(x, "x"), _dev_tensor(w, "w"), _dev_tensor(dy, "dy")
         K = _conv_shape(x, w, 3)
         Bn, T, D = x.shape
@@ -127,7 +172,7 @@ def mi_causal_conv_bwd(x, w, bias, x0, dy, dxT=None, *, act=None, lengths=None, 
 def mi_causal_conv_step(x, w, bias, x0, *, act=None, y=None, x_out=None, stream=None):
     """(y, x_out): one step, x (B, D) with the carried inputs x0 (B, K-1, D).
     x_out (default: a new tensor) may be x0 itself, which is then updated in place."""
-    with _Call(stream, _device(x, "x")) as c:
+    with _call(stream, _device(x, "x")) as c:
         x, w = _dev_tensor(x, "x"), _dev_tensor(w, "w")
         K = _conv_shape(x, w, 2)
         Bn, D = x.shape
@@ -169,7 +214,8 @@ def _scan_args(u, delta, A, Bm, Cm, skip, z, delta_bias, dims):
         raise ValueError("G = %d must divide D = %d" % (G, D))
     delta = _need(delta, u, u.shape, "delta")
     Cm = _need(Cm, u, Bm.shape, "Cm")
-    _same(u, Bm)
+    if Bm.dtype != u.dtype or Bm.device != u.device:
+        raise ValueError("u, delta, Bm, Cm and z must share device and dtype (%s, %s)" % (u.device, u.dtype))
     skip, delta_bias = _opt(skip, u, (D,), "skip", _F32), _opt(delta_bias, u, (D,), "delta_bias", _F32)
     z = _opt(z, u, u.shape, "z")
     T = u.shape[1] if dims == 3 else 1
@@ -182,7 +228,7 @@ def mi_selective_scan_fwd(u, delta, A, Bm, Cm, skip=None, z=None, delta_bias=Non
     softplus(delta + delta_bias), A (D, N), Bm, Cm (B, T, G, N), y gated by
     silu(z), from the state h0 (B, D, N) to hT.  `states` is what the backward
     needs, or None unless save_states is set (or a tensor for it is given)."""
-    with _Call(stream, _device(u, "u")) as c:
+    with _call(stream, _device(u, "u")) as c:
         args, (Bn, T, D, G, N) = _scan_args(u, delta, A, Bm, Cm, skip, z, delta_bias, 3)
         u = args[0]
         h0 = _opt(h0, u, (Bn, D, N), "h0", _F32)
@@ -209,7 +255,7 @@ def mi_selective_scan_bwd(u, delta, A, Bm, Cm, states, dy, dhT=None, skip=None, 
     """(du, ddelta, dA, dBm, dCm, dskip, dz, ddelta_bias, dh0): gradient of
     mi_selective_scan_fwd for dy (B, T, D) and, optionally, dhT (B, D, N), given
     the forward's `states`; None for inputs that were None."""
-    with _Call(stream, _device(u, "u")) as c:
+    with _call(stream, _device(u, "u")) as c:
         args, (Bn, T, D, G, N) = _scan_args(u, delta, A, Bm, Cm, skip, z, delta_bias, 3)
         u, delta, A, Bm, Cm, skip, z, delta_bias = args
         blk = max(1, mi_selective_scan_block(N))
@@ -238,7 +284,7 @@ def mi_selective_scan_step(u, delta, A, Bm, Cm, h, skip=None, z=None, delta_bias
     """(y, h_out): one step, u, delta, z (B, D), Bm, Cm (B, G, N), from the state
     h (B, D, N).  h_out (default: a new tensor) may be h itself, which is then
     updated in place."""
-    with _Call(stream, _device(u, "u")) as c:
+    with _call(stream, _device(u, "u")) as c:
         args, (Bn, _, D, G, N) = _scan_args(u, delta, A, Bm, Cm, skip, z, delta_bias, 2)
         u, delta, A, Bm, Cm, skip, z, delta_bias = args
         own = h
@@ -281,7 +327,7 @@ def mi_group_norm_fwd(x, w=None, bias=None, z=None, *, groups=1, eps=1e-5, cente
     """y: x (..., D) normalised over the D / groups channels of each group of
     each row (mean and variance, or the root mean square if not centered), times
     w plus bias, through `act` or gated by silu(z)."""
-    with _Call(stream, _device(x, "x")) as c:
+    with _call(stream, _device(x, "x")) as c:
         x, w, bias, z, R, D = _norm_args(x, w, bias, z, groups, act)
         y = _out(y, x, "y")
         c.keep(x, w, bias, z, y)
@@ -300,7 +346,7 @@ def mi_group_norm_bwd(x, w, bias, dy, z=None, *, groups=1, eps=1e-5, centered=Tr
                       stream=None):
     """(dx, dw, dbias, dz): gradient of mi_group_norm_fwd for dy (..., D); None
     for inputs that were None."""
-    with _Call(stream, _device(x, "x")) as c:
+    with _call(stream, _device(x, "x")) as c:
         x, w, bias, z, R, D = _norm_args(x, w, bias, z, groups, act)
         dy = _need(dy, x, x.shape, "dy")
         dx = _out(dx, x, "dx")

@@ -253,41 +253,89 @@ __global__ __launch_bounds__(NW * 64, WPS) void scan_fwd_kernel(ScanArgs p) {
             if (st_off[f] >= 0) p.hT[st_base + st_off[f]] = carry[f];
 }
 
-// One token: a lane owns up to four states of a channel, LQ lanes a channel.
-// The state is read and written once, which is nearly all the traffic.
-template <typename T>
-__global__ __launch_bounds__(256) void scan_step_kernel(ScanArgs p, int lq, int64_t n_ch) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t chan = i / lq;  // b * D + d
-    const int q = (int)(i % lq);
-    const bool live = chan < n_ch;
-    float acc = 0.f;
-    int64_t b = 0, d = 0;
-    if (live) {
-        b = chan / p.D;
-        d = chan - b * p.D;
-        const float uu = ld1(static_cast<const T *>(p.u) + chan);
-        const float raw = ld1(static_cast<const T *>(p.delta) + chan) + (p.delta_bias ? p.delta_bias[d] : 0.f);
-        const float dl = gate_rate(raw, p.softplus, nullptr);
-        const float x = dl * uu;
-        const int64_t brow = (b * p.G + d / p.per) * p.N;
+// One token: a lane owns up to four states of a channel, LQ lanes a channel, a
+// workgroup 256 / LQ channels of one sequence.  The state is read and written
+// once, which is nearly all the traffic: the bound is HBM.  QUAD: rows of whole,
+// aligned quads.
+template <typename T, int LQ, bool QUAD>
+__global__ __launch_bounds__(256) void scan_step_kernel(ScanArgs p, int wg_row) {
+    const int64_t b = blockIdx.x / wg_row;
+    const int c = (int)(blockIdx.x - (int)b * wg_row) * (256 / LQ) + (int)threadIdx.x / LQ;
+    const int q = (int)threadIdx.x % LQ;
+    const bool live = c < p.D;
+    const int64_t d = live ? c : 0, chan = b * p.D + d;
+    const int N = (int)p.N, n0 = 4 * q;
+    const int nv = !live ? 0 : N - n0 < 0 ? 0 : N - n0 > 4 ? 4 : N - n0;
+    const int64_t brow = (b * p.G + (p.G > 1 ? (int)d / p.per : 0)) * N + n0;
+    float h[4], A[4], Bv[4], Cv[4];
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            const int64_t n = q * 4 + s;
-            if (n < p.N) {
-                const float a = __builtin_amdgcn_exp2f(dl * (p.A[d * p.N + n] * LOG2E));
-                const float h = fmaf(a, p.h0[chan * p.N + n], x * ld1(static_cast<const T *>(p.Bm) + brow + n));
-                p.hT[chan * p.N + n] = h;
-                acc = fmaf(ld1(static_cast<const T *>(p.Cm) + brow + n), h, acc);
-            }
+    for (int s = 0; s < 4; ++s) h[s] = A[s] = Bv[s] = Cv[s] = 0.f;
+    const float *hp = p.h0 + chan * N + n0, *ap = p.A + d * N + n0;
+    const T *bp = static_cast<const T *>(p.Bm) + brow, *cp = static_cast<const T *>(p.Cm) + brow;
+    if (QUAD) {
+        if (nv > 0) {
+            Pack<float, 4>::unpack(load_vec<float, 4>(hp), h);
+            Pack<float, 4>::unpack(load_vec<float, 4>(ap), A);
+            Pack<T, 4>::unpack(load_vec<T, 4>(bp), Bv);
+            Pack<T, 4>::unpack(load_vec<T, 4>(cp), Cv);
         }
-        if (q == 0 && p.skip) acc = fmaf(p.skip[d], uu, acc);
+    } else {
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+            if (s < nv) {
+                h[s] = hp[s];
+                A[s] = ap[s];
+                Bv[s] = ld1(bp + s);
+                Cv[s] = ld1(cp + s);
+            }
     }
-    for (int m = 1; m < lq; m *= 2) acc += __shfl_xor(acc, m);
+    const float uu = ld1(static_cast<const T *>(p.u) + chan);
+    const float raw = ld1(static_cast<const T *>(p.delta) + chan) + (p.delta_bias ? p.delta_bias[d] : 0.f);
+    const float zz = p.z ? ld1(static_cast<const T *>(p.z) + chan) : 0.f;
+    const float dl = gate_rate(raw, p.softplus, nullptr);
+    float acc = 0.f;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+        h[s] = fmaf(__builtin_amdgcn_exp2f(dl * (A[s] * LOG2E)), h[s], dl * uu * Bv[s]);
+        acc = fmaf(Cv[s], h[s], acc);
+    }
+    float *ho = p.hT + chan * N + n0;
+    if (QUAD) {
+        if (nv > 0) *reinterpret_cast<f32x4 *>(ho) = Pack<float, 4>::pack(h);
+    } else {
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+            if (s < nv) ho[s] = h[s];
+    }
+#pragma unroll
+    for (int m = 1; m < LQ; m *= 2) acc += __shfl_xor(acc, m);
     if (live && q == 0) {
-        if (p.z) acc *= silu(ld1(static_cast<const T *>(p.z) + chan));
+        if (p.skip) acc = fmaf(p.skip[d], uu, acc);
+        if (p.z) acc *= silu(zz);
         st1(static_cast<T *>(p.y) + chan, acc);
     }
+}
+
+template <typename T, int LQ>
+mi_status launch_step(const ScanArgs &a, bool quad, hipStream_t s) {
+    const int64_t wg_row = (a.D + 256 / LQ - 1) / (256 / LQ);
+    int64_t grid;
+    if (!mul_ok(a.B, wg_row, 1, 1, &grid) || grid > 0x7fffffff) return MI_ERR_UNSUPPORTED;
+    const dim3 gd((unsigned)grid), bd(256);
+    if (quad) hipLaunchKernelGGL((scan_step_kernel<T, LQ, true>), gd, bd, 0, s, a, (int)wg_row);
+    else hipLaunchKernelGGL((scan_step_kernel<T, LQ, false>), gd, bd, 0, s, a, (int)wg_row);
+    return launch_status();
+}
+template <typename T>
+mi_status launch_step_t(const ScanArgs &a, hipStream_t s) {
+    const auto at = [](const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; };
+    const bool quad = a.N % 4 == 0 && at(a.h0, 16) && at(a.hT, 16) && at(a.A, 16) && at(a.Bm, 4 * sizeof(T)) &&
+                      at(a.Cm, 4 * sizeof(T));
+    if (a.N <= 4) return launch_step<T, 1>(a, quad, s);
+    if (a.N <= 8) return launch_step<T, 2>(a, quad, s);
+    if (a.N <= 16) return launch_step<T, 4>(a, quad, s);
+    if (a.N <= 32) return launch_step<T, 8>(a, quad, s);
+    return launch_step<T, 16>(a, quad, s);
 }
 
 template <typename T, int S, int C, int L, int NW, int WPS>
@@ -408,15 +456,9 @@ mi_status mi_selective_scan_step(const void *u, const void *delta, const float *
     a.B = B; a.T = 1; a.D = D; a.N = N; a.softplus = softplus_on != 0;
     if (D > SCAN_MAX_D || G * N > SCAN_MAX_D) return MI_ERR_UNSUPPORTED;
     a.G = (int)G; a.per = (int)(D / G);
-    int lq = 1;
-    while (lq * 4 < N) lq *= 2;
-    const int64_t grid = (B * D * lq + 255) / 256;
-    if (grid > 0x7fffffff) return MI_ERR_UNSUPPORTED;
-    const dim3 gd((unsigned)grid), bd(256);
-    if (dt == MI_F32) hipLaunchKernelGGL(scan_step_kernel<float>, gd, bd, 0, stream, a, lq, B * D);
-    else if (dt == MI_BF16) hipLaunchKernelGGL(scan_step_kernel<bf16_t>, gd, bd, 0, stream, a, lq, B * D);
-    else hipLaunchKernelGGL(scan_step_kernel<f16_t>, gd, bd, 0, stream, a, lq, B * D);
-    return launch_status();
+    if (dt == MI_F32) return launch_step_t<float>(a, stream);
+    if (dt == MI_BF16) return launch_step_t<bf16_t>(a, stream);
+    return launch_step_t<f16_t>(a, stream);
 }
 
 }  // extern "C"
