@@ -285,14 +285,17 @@ mi_status mi_causal_conv_step(const void *x, const float *w, const float *bias, 
  *     s_t = sum_n Cm_t[n] h_t[n] + skip u_t,   y_t = s_t silu(z_t)
  * hT is the state at the sequence's length.  `states`, or NULL, receives what
  * the backward needs: the fp32 state before every block of
- * mi_selective_scan_block(N) steps, (B, ceil(T/block), D, N). */
+ * mi_selective_scan_block(N) steps, (B, ceil(T/block), D, N).  The workspace
+ * holds the transforms of a sequence's segments where the channels alone do
+ * not fill the GPU; it may be NULL where the query says 0 bytes. */
 int64_t mi_selective_scan_block(int64_t N);
+size_t mi_selective_scan_fwd_workspace(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N, mi_dtype dt);
 mi_status mi_selective_scan_fwd(const void *u, const void *delta, const float *A, const void *Bm,
                                 const void *Cm, const float *skip, const void *z,
                                 const float *delta_bias, const float *h0, const int32_t *lengths,
                                 void *y, float *hT, float *states, int64_t B, int64_t T, int64_t D,
-                                int64_t G, int64_t N, int softplus, mi_dtype dt,
-                                hipStream_t stream);
+                                int64_t G, int64_t N, int softplus, mi_dtype dt, void *ws,
+                                size_t ws_bytes, hipStream_t stream);
 
 /* Gradient for the upstream gradients dy (B,T,D) and dhT (B,D,N) or NULL.
  * `states` is the forward's.  dskip, dz, ddelta_bias go with skip, z and

@@ -67,7 +67,8 @@ _SIGS = {
     "mi_causal_conv_bwd": ([_V] * 11 + [_I64] * 4 + [_I, _I, _V, _SZ, _V], _I),
     "mi_causal_conv_step": ([_V] * 6 + [_I64] * 3 + [_I, _I, _V], _I),
     "mi_selective_scan_block": ([_I64], _I64),
-    "mi_selective_scan_fwd": ([_V] * 13 + [_I64] * 5 + [_I, _I, _V], _I),
+    "mi_selective_scan_fwd_workspace": ([_I64] * 5 + [_I], _SZ),
+    "mi_selective_scan_fwd": ([_V] * 13 + [_I64] * 5 + [_I, _I, _V, _SZ, _V], _I),
     "mi_selective_scan_bwd_workspace": ([_I64] * 5 + [_I], _SZ),
     "mi_selective_scan_bwd": ([_V] * 21 + [_I64] * 5 + [_I, _I, _V, _SZ, _V], _I),
     "mi_selective_scan_step": ([_V] * 11 + [_I64] * 4 + [_I, _I, _V], _I),

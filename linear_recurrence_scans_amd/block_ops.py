@@ -17,7 +17,7 @@ from . import _Call, _check, _device, _dt, _load, _workspace
 
 __all__ = [
     "mi_causal_conv_fwd", "mi_causal_conv_bwd", "mi_causal_conv_bwd_workspace", "mi_causal_conv_step",
-    "mi_selective_scan_block", "mi_selective_scan_fwd", "mi_selective_scan_bwd", "mi_selective_scan_bwd_workspace",
+    "mi_selective_scan_block", "mi_selective_scan_fwd_workspace", "mi_selective_scan_fwd", "mi_selective_scan_bwd", "mi_selective_scan_bwd_workspace",
     "mi_selective_scan_step",
     "mi_group_norm_fwd", "mi_group_norm_bwd", "mi_group_norm_bwd_workspace",
 ]
@@ -222,8 +222,13 @@ def _scan_args(u, delta, A, Bm, Cm, skip, z, delta_bias, dims):
     return (u, delta, A, Bm, Cm, skip, z, delta_bias), (u.shape[0], T, D, G, N)
 
 
+def mi_selective_scan_fwd_workspace(B: int, T: int, D: int, G: int, N: int, dtype=torch.float32) -> int:
+    from . import _DTYPES
+    return int(_load().mi_selective_scan_fwd_workspace(B, T, D, G, N, _DTYPES[dtype]))
+
+
 def mi_selective_scan_fwd(u, delta, A, Bm, Cm, skip=None, z=None, delta_bias=None, h0=None, *, softplus=True,
-                          lengths=None, save_states=False, y=None, hT=None, states=None, stream=None):
+                          lengths=None, save_states=False, y=None, hT=None, states=None, ws=None, stream=None):
     """(y, hT, states): the selective scan of u (B, T, D) with rates
     softplus(delta + delta_bias), A (D, N), Bm, Cm (B, T, G, N), y gated by
     silu(z), from the state h0 (B, D, N) to hT.  `states` is what the backward
@@ -237,10 +242,12 @@ def mi_selective_scan_fwd(u, delta, A, Bm, Cm, skip=None, z=None, delta_bias=Non
         if save_states or states is not None:
             blk = max(1, mi_selective_scan_block(N))
             states = _new(states, u, (Bn, (T + blk - 1) // blk, D, N), "states", _F32)
-        c.keep(*args, h0, lengths, y, hT, states)
-        st = _load().mi_selective_scan_fwd(*(_ptr(t) for t in args), _ptr(h0), _ptr(lengths), y.data_ptr(),
-                                           hT.data_ptr(), _ptr(states), Bn, T, D, G, N, int(bool(softplus)),
-                                           _dt(u), c.handle)
+        lib, dt = _load(), _dt(u)
+        ws = _workspace(ws, lib.mi_selective_scan_fwd_workspace(Bn, T, D, G, N, dt), u.device)
+        c.keep(*args, h0, lengths, y, hT, states, ws)
+        st = lib.mi_selective_scan_fwd(*(_ptr(t) for t in args), _ptr(h0), _ptr(lengths), y.data_ptr(),
+                                       hT.data_ptr(), _ptr(states), Bn, T, D, G, N, int(bool(softplus)), dt,
+                                       ws.data_ptr(), _nbytes(ws), c.handle)
         _check(st, "mi_selective_scan_fwd")
     return y, hT, states
 

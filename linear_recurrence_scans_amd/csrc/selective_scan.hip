@@ -13,7 +13,9 @@
 namespace miscan {
 namespace {
 
-template <typename T, int S, int C, int L, int NW, int WPS>
+// SUM: the first kernel of a cut sequence, which only forms its segment's
+// transform.
+template <typename T, int S, int C, int L, int NW, int WPS, bool SUM>
 __global__ __launch_bounds__(NW * 64, WPS) void scan_fwd_kernel(ScanArgs p) {
     constexpr int EL = S * C, J = L / 4, NP = 4 * S;
     constexpr int E = EL * 64;                      // states a tile
@@ -38,7 +40,9 @@ __global__ __launch_bounds__(NW * 64, WPS) void scan_fwd_kernel(ScanArgs p) {
     const int sg = lane >> 4, cl = lane & 15;
     const int tile = item % p.tiles;
     const int g = item / p.tiles % p.G;
-    const int64_t b = item / p.tiles / p.G;
+    const int64_t b = item / p.tiles / p.G % (int)p.B;
+    const int seg = item / p.tiles / p.G / (int)p.B;
+    const int64_t t_first = seg * p.seg, t_last = t_first + p.seg < p.T ? t_first + p.seg : p.T;
     const int ch0 = tile * 16 * C;                  // first channel of the tile inside its group
     const int64_t d0 = (int64_t)g * p.per + ch0;
     const int nch = p.per - ch0 < 16 * C ? p.per - ch0 : 16 * C;
@@ -59,7 +63,7 @@ __global__ __launch_bounds__(NW * 64, WPS) void scan_fwd_kernel(ScanArgs p) {
         }
     }
     // folded states: thread tid carries positions tid, tid + NT, ... of the tile
-    float carry[FPT];
+    float carry[FPT], prod[FPT];
     int st_off[FPT];  // offset from the tile's first state, or -1
     const int64_t st_base = b * p.D * p.N + d0 * p.N;
 #pragma unroll
@@ -69,7 +73,14 @@ __global__ __launch_bounds__(NW * 64, WPS) void scan_fwd_kernel(ScanArgs p) {
         LV::where(i < E ? i : 0, &ln, &e);
         const int n = (ln >> 4) * S + e % S, ch = (ln & 15) * C + e / S;
         st_off[f] = i < E && n < p.N && ch < nch ? ch * (int)p.N + n : -1;
-        carry[f] = st_off[f] >= 0 && p.h0 ? p.h0[st_base + st_off[f]] : 0.f;
+        carry[f] = !SUM && st_off[f] >= 0 && p.h0 ? p.h0[st_base + st_off[f]] : 0.f;
+        if (!SUM && st_off[f] >= 0) {
+            const float *v = p.seg_v + st_base + st_off[f], *q = p.seg_p + st_base + st_off[f];
+#pragma unroll 4
+            for (int k = 0; k < seg; ++k)
+                carry[f] = fmaf(q[k * p.B * p.D * p.N], carry[f], v[k * p.B * p.D * p.N]);
+        }
+        prod[f] = 1.f;
     }
     // a lane's rows: steps sg, 4 + sg, ... of the wave's, as byte offsets from the wave's first
     const uint32_t row = (uint32_t)(p.D * (int64_t)sizeof(T));
@@ -93,7 +104,7 @@ __global__ __launch_bounds__(NW * 64, WPS) void scan_fwd_kernel(ScanArgs p) {
         load_rows<T, C, J>(make_rows(static_cast<const T *>(p.u) + row0 + t0 * p.D, left * row), voff, nv, whole, ur);
         load_rows<T, C, J>(make_rows(static_cast<const T *>(p.delta) + row0 + t0 * p.D, left * row), voff, nv, whole,
                            dr);
-        if (p.z)
+        if (!SUM && p.z)
             load_rows<T, C, J>(make_rows(static_cast<const T *>(p.z) + row0 + t0 * p.D, left * row), voff, nv, whole,
                                zr);
         const rsrc_t rb = make_rows(static_cast<const T *>(p.Bm) + b0 + t0 * brow, left * brow * (int64_t)sizeof(T));
@@ -101,12 +112,12 @@ __global__ __launch_bounds__(NW * 64, WPS) void scan_fwd_kernel(ScanArgs p) {
 #pragma unroll
         for (int i = 0; i < BPL; ++i) {
             br[i] = buf_read<T, 1>(rb, boff[i]);
-            cr[i] = buf_read<T, 1>(rc, boff[i]);
+            if (!SUM) cr[i] = buf_read<T, 1>(rc, boff[i]);
         }
     };
 
-    load((int64_t)wave * L);
-    for (int64_t tb = 0; tb < p.T; tb += NW * L) {
+    load(t_first + wave * L);
+    for (int64_t tb = t_first; tb < t_last; tb += NW * L) {
         const int64_t t0 = tb + wave * L;
         const int left = steps_left<L>(t0, len);
         // this wave's rows: dl and dl u by the lanes that own them
@@ -133,10 +144,10 @@ __global__ __launch_bounds__(NW * 64, WPS) void scan_fwd_kernel(ScanArgs p) {
             const int q = lane + 64 * i, t = q / NP, n = q % NP;
             if (L * NP % 64 == 0 || q < L * NP) {
                 Pack<T, 1>::unpack(br[i], &sm_b[wave][n][t]);
-                Pack<T, 1>::unpack(cr[i], &sm_c[wave][t][n]);
+                if (!SUM) Pack<T, 1>::unpack(cr[i], &sm_c[wave][t][n]);
             }
         }
-        if (tb + NW * L < p.T) load(t0 + NW * L);
+        if (tb + NW * L < t_last) load(t0 + NW * L);
         wave_lds_sync();
         // the wave's steps from a zero state
         float a[L][S][C], h[S][C], yl[L][C], sum[C];
@@ -158,7 +169,7 @@ __global__ __launch_bounds__(NW * 64, WPS) void scan_fwd_kernel(ScanArgs p) {
                 __builtin_amdgcn_sched_barrier(0);
                 float dx[2 * C], bt[NB], ct[S];
                 lds_read<2 * C>(sm_x[wave][t][cl], dx);
-                lds_read<S>(&sm_c[wave][t][sg * S], ct);
+                if constexpr (!SUM) lds_read<S>(&sm_c[wave][t][sg * S], ct);
 #pragma unroll
                 for (int i = 0; i < NB; ++i) bt[i] = bq[i][k];
 #pragma unroll
@@ -168,13 +179,21 @@ __global__ __launch_bounds__(NW * 64, WPS) void scan_fwd_kernel(ScanArgs p) {
                     const float bs = QR::template get<s>(bt);
 #pragma unroll
                     for (int c = 0; c < C; ++c) {
-                        a[t][s][c] = __builtin_amdgcn_exp2f(dx[c] * A2[s][c]);
+                        const float gate = __builtin_amdgcn_exp2f(dx[c] * A2[s][c]);
                         const float x = bs * dx[C + c];
-                        h[s][c] = t == 0 ? x : fmaf(a[t][s][c], h[s][c], x);
-                        yl[t][c] = fmaf(ct[s], h[s][c], yl[t][c]);
+                        h[s][c] = t == 0 ? x : fmaf(gate, h[s][c], x);
+                        if constexpr (!SUM) {
+                            a[t][s][c] = gate;
+                            yl[t][c] = fmaf(ct[s], h[s][c], yl[t][c]);
+                        }
                     }
                 });
-                pin(yl[t]);
+                if constexpr (!SUM) {
+                    pin(yl[t]);
+                } else {
+#pragma unroll
+                    for (int s = 0; s < S; ++s) pin(h[s]);
+                }
             }
         }
         float hv[EL], pv[EL];
@@ -200,6 +219,11 @@ __global__ __launch_bounds__(NW * 64, WPS) void scan_fwd_kernel(ScanArgs p) {
                 }
 #pragma unroll
                 for (int w = 0; w < NW; ++w) {
+                    if (SUM) {
+                        prod[f] *= pw[w];
+                        c = fmaf(pw[w], c, sv[w]);
+                        continue;
+                    }
                     if ((w * L) % scan_block_of<S>() % (NW * L) == 0 && (tb + w * L) % scan_block_of<S>() == 0 &&
                         p.states && st_off[f] >= 0 && tb + w * L < p.T) {
                         const int64_t blk = (tb + w * L) / scan_block_of<S>();
@@ -213,6 +237,7 @@ __global__ __launch_bounds__(NW * 64, WPS) void scan_fwd_kernel(ScanArgs p) {
             }
         }
         wg_lds_sync();
+        if constexpr (SUM) continue;
         // the state that entered the wave, carried through its gates
         LV::read(sm_s[wave], lane, hv);
 #pragma unroll
@@ -247,7 +272,17 @@ __global__ __launch_bounds__(NW * 64, WPS) void scan_fwd_kernel(ScanArgs p) {
             if (4 * j + sg < rows) store_ch<T, C>(y + voff[j], nv, whole, o);
         }
     }
-    if (p.hT)
+    if constexpr (SUM) {
+#pragma unroll
+        for (int f = 0; f < FPT; ++f)
+            if (st_off[f] >= 0) {
+                const int64_t at = seg * p.B * p.D * p.N + st_base + st_off[f];
+                p.seg_v[at] = carry[f];
+                p.seg_p[at] = prod[f];
+            }
+        return;
+    }
+    if (p.hT && seg == p.n_seg - 1)
 #pragma unroll
         for (int f = 0; f < FPT; ++f)
             if (st_off[f] >= 0) p.hT[st_base + st_off[f]] = carry[f];
@@ -338,34 +373,74 @@ mi_status launch_step_t(const ScanArgs &a, hipStream_t s) {
     return launch_step<T, 16>(a, quad, s);
 }
 
-template <typename T, int S, int C, int L, int NW, int WPS>
-mi_status launch_tile(ScanArgs a, hipStream_t s) {
+template <typename T, int S, int C, int L, int NW, int WPS, bool CUT>
+mi_status launch_tile(ScanArgs a, int64_t n_seg, hipStream_t s) {
     a.tiles = (a.per + 16 * C - 1) / (16 * C);
     int64_t items;
-    if (!mul_ok(a.B, a.G, a.tiles, 1, &items) || items > 0x7ffffff0) return MI_ERR_UNSUPPORTED;
+    if (!mul_ok(a.B, a.G, a.tiles, n_seg, &items) || items > 0x7ffffff0) return MI_ERR_UNSUPPORTED;
+    a.n_seg = (int)n_seg;
+    a.seg = (a.T + NW * L * n_seg - 1) / (NW * L * n_seg) * (NW * L);
+    if constexpr (CUT)
+        if (n_seg > 1) {
+            a.n_items = (int)(items / n_seg * (n_seg - 1));  // nothing needs the last segment's transform
+            hipLaunchKernelGGL((scan_fwd_kernel<T, S, C, L, NW, WPS, true>), dim3(xcd_grid(a.n_items)),
+                               dim3(NW * 64), 0, s, a);
+            const mi_status st = launch_status();
+            if (st != MI_OK) return st;
+        }
     a.n_items = (int)items;
-    hipLaunchKernelGGL((scan_fwd_kernel<T, S, C, L, NW, WPS>), dim3(xcd_grid(a.n_items)), dim3(NW * 64), 0, s, a);
+    hipLaunchKernelGGL((scan_fwd_kernel<T, S, C, L, NW, WPS, false>), dim3(xcd_grid(a.n_items)), dim3(NW * 64), 0, s,
+                       a);
     return launch_status();
 }
 
-// Tile of a call, by the number of workgroups that its wide tiles make.
+// How a call is cut, by the number of workgroups that its channel tiles make.
 //  - 768 or more (three a CU): workgroups of 4 waves at 3 waves a SIMD, which
 //    overlap each other's folds; B = 8, T = 4096, D = 4096, N = 16, bf16 (1024):
 //    744 us, against 892 with 8 waves.
 //  - fewer: 8 waves, so that a workgroup a CU still fills half of it; B = 2, T =
-//    4096, D = 4096 with z (256): 237 us, against 349 with 4 waves.
-//  - fewer than 256: narrow tiles (one channel a lane) of 16 waves: twice the
-//    workgroups and four times the waves; B = 1, T = 8192, D = 4096 with z (128):
-//    251 us, against 456 with wide tiles of 8 waves.  At 256 both take the same
-//    (249 and 237).
+//    4096, D = 4096 with z (256): 225 us, against 349 with 4 waves.
+//  - fewer than 256: narrow tiles (one channel a lane) of 16 waves, while those
+//    make at least 192 workgroups: four times the waves; B = 1, T = 8192, D = 4096
+//    with z (128 wide, 256 narrow): 245 us, against 456 with wide tiles of 8 waves.
+//  - fewer still: segments of the sequence, as many as make 768 workgroups of 4
+//    waves.
+enum FwdCut { FWD_MANY, FWD_EIGHT, FWD_NARROW, FWD_SEGMENTS };
+struct FwdPlan {
+    FwdCut cut;
+    int64_t n_seg;
+};
+template <int S>
+FwdPlan fwd_plan(int64_t B, int64_t G, int64_t per, int64_t T) {
+    constexpr int C = FwdTile<S>::C, L = FwdTile<S>::L;
+    const int64_t n = B * G * ((per + 16 * C - 1) / (16 * C)), narrow = B * G * ((per + 15) / 16);
+    if (n >= 768) return {FWD_MANY, 1};
+    if (n >= 256) return {FWD_EIGHT, 1};
+    if (S < 16 && narrow >= 192) return {FWD_NARROW, 1};
+    const int64_t blocks = (T + 4 * L - 1) / (4 * L), want = (768 + n - 1) / n;
+    const int64_t seg = (blocks + want - 1) / want;  // blocks a segment
+    return {FWD_SEGMENTS, blocks < 2 || seg < 1 ? 1 : (blocks + seg - 1) / seg};
+}
+int64_t fwd_segments(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N) {
+    switch (scan_s(N)) {
+        case 1: return fwd_plan<1>(B, G, D / G, T).n_seg;
+        case 2: return fwd_plan<2>(B, G, D / G, T).n_seg;
+        case 4: return fwd_plan<4>(B, G, D / G, T).n_seg;
+        case 8: return fwd_plan<8>(B, G, D / G, T).n_seg;
+    }
+    return fwd_plan<16>(B, G, D / G, T).n_seg;
+}
+
 template <typename T, int S>
 mi_status launch_fwd(const ScanArgs &a, hipStream_t s) {
     constexpr int C = FwdTile<S>::C, L = FwdTile<S>::L;
-    constexpr int LN = S >= 8 ? 4 : S >= 2 ? 8 : 16;  // at most 32 gates a lane: 128 registers (64 gates for S = 16)
-    const int64_t n = a.B * a.G * ((a.per + 16 * C - 1) / (16 * C));
-    if (n >= 768) return launch_tile<T, S, C, L, 4, S == 2 || S == 16 ? 2 : 3>(a, s);
-    if (n >= 256 || S == 16) return launch_tile<T, S, C, L, 8, 2>(a, s);
-    return launch_tile<T, S, 1, LN, S == 16 ? 8 : 16, S == 16 ? 2 : 4>(a, s);
+    constexpr int WPS = S == 16 ? 2 : 3;
+    constexpr int LN = S >= 8 ? 4 : S >= 2 ? 8 : 16;  // narrow: at most 32 gates a lane, 128 registers
+    const FwdPlan q = fwd_plan<S>(a.B, a.G, a.per, a.T);
+    if (q.cut == FWD_EIGHT) return launch_tile<T, S, C, L, 8, 2, false>(a, 1, s);
+    if constexpr (S < 16)
+        if (q.cut == FWD_NARROW) return launch_tile<T, S, 1, LN, 16, 4, false>(a, 1, s);
+    return launch_tile<T, S, C, L, 4, WPS, true>(a, q.n_seg, s);
 }
 template <typename T>
 mi_status launch_fwd_t(const ScanArgs &a, hipStream_t s) {
@@ -410,10 +485,19 @@ extern "C" {
 
 int64_t mi_selective_scan_block(int64_t N) { return N < 1 || N > 64 ? 0 : scan_block(N); }
 
+size_t mi_selective_scan_fwd_workspace(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N, mi_dtype dt) {
+    ScanSizes s;
+    if (check_scan(B, T, D, G, N, dt, &s) != MI_OK || B == 0 || T == 0 || D == 0) return 0;
+    const int64_t n = fwd_segments(B, T, D, G, N);
+    int64_t bytes;
+    return n > 1 && mul_ok(s.h, n, 2, 1, &bytes) ? (size_t)bytes : 0;
+}
+
 mi_status mi_selective_scan_fwd(const void *u, const void *delta, const float *A, const void *Bm, const void *Cm,
                                 const float *skip, const void *z, const float *delta_bias, const float *h0,
                                 const int32_t *lengths, void *y, float *hT, float *states, int64_t B, int64_t T,
-                                int64_t D, int64_t G, int64_t N, int softplus_on, mi_dtype dt, hipStream_t stream) {
+                                int64_t D, int64_t G, int64_t N, int softplus_on, mi_dtype dt, void *ws,
+                                size_t ws_bytes, hipStream_t stream) {
     ScanSizes s;
     mi_status st = check_scan(B, T, D, G, N, dt, &s);
     if (st != MI_OK) return st;
@@ -428,6 +512,12 @@ mi_status mi_selective_scan_fwd(const void *u, const void *delta, const float *A
     a.u = u; a.delta = delta; a.z = z; a.Bm = Bm; a.Cm = Cm; a.A = A; a.skip = skip; a.delta_bias = delta_bias;
     a.h0 = h0; a.lengths = lengths; a.y = y; a.hT = hT; a.states = states;
     a.B = B; a.T = T; a.D = D; a.N = N; a.softplus = softplus_on != 0;
+    const size_t need = mi_selective_scan_fwd_workspace(B, T, D, G, N, dt);
+    if (need > 0) {
+        if ((st = check_ws_lists(ws, ws_bytes, need, in, out)) != MI_OK) return st;
+        a.seg_v = static_cast<float *>(ws);
+        a.seg_p = a.seg_v + need / 8;
+    }
     if (D > SCAN_MAX_D || G * N > SCAN_MAX_D) return MI_ERR_UNSUPPORTED;
     a.G = (int)G; a.per = (int)(D / G);
     a.vec = scan_vec(a, dt);

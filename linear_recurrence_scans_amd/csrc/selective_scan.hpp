@@ -8,6 +8,13 @@
 // through softplus and gated by one lane only, and the joined sums land on the
 // lane that needs them.
 //
+// Few channels.  Where the channel tiles do not fill the GPU, the sequence is cut
+// into segments with a workgroup each: a first kernel forms every segment's
+// transform (gates' product P, scan from zero), and a workgroup of the second
+// folds those before (in the backward: after) its own, in order, to what enters
+// its segment.  The gates are then formed twice, 17 issue slots a state-step
+// instead of 12, on as many CUs as there are.
+//
 // Time.  A workgroup walks the sequence of one channel tile in blocks of NW L
 // steps; wave w scans steps [w L, (w + 1) L) of the block from a zero state,
 // the per-wave transforms (P, S) meet in LDS, where the carries are folded, and
@@ -32,11 +39,14 @@ struct ScanArgs {
     void *du, *ddelta, *dz;
     float *dh0;
     float *part_bc;        // (tiles a group, 2, B, T, G, N) partial dBm, dCm
-    float *part_a;         // (B, N + 2, D) partial dA (transposed), dskip, ddelta_bias
+    float *part_a;         // (B * n_seg, N + 2, D) partial dA (transposed), dskip, ddelta_bias
     int64_t B, T, D, N;
     int G, per;            // groups, channels a group
     int tiles;             // channel tiles a group
-    int n_items;           // B * G * tiles
+    int n_seg;             // segments of the sequence, one workgroup each
+    int64_t seg;           // steps a segment: whole blocks
+    float *seg_v, *seg_p;  // (n_seg, B, D, N) transform of a segment: its scan from zero, its gates' product
+    int n_items;           // n_seg * B * G * tiles
     int softplus;
     int vec;               // rows may be read C channels at a time
 };

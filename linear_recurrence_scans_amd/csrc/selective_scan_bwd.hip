@@ -78,6 +78,158 @@ __device__ __forceinline__ void join_channels(const float (*red)[ROW], int lane,
     }
 }
 
+// The first kernel of a cut sequence: every segment's reverse transform, the
+// gradient that leaves its left end for none entering at its right, and the
+// product of its gates.
+template <typename T, int S, int C, int L, int NW>
+__global__ __launch_bounds__(NW * 64) void scan_bwd_sum_kernel(ScanArgs p) {
+    constexpr int EL = S * C, J = L / 4, NP = 4 * S;
+    constexpr int E = EL * 64, NT = NW * 64, FPT = (E + NT - 1) / NT, BPL = (L * NP + 63) / 64;
+    using LV = LaneVec<EL>;
+    using PC = Pack<T, C>;
+    using raw_t = typename PC::raw_t;
+    using one_t = typename Pack<T, 1>::raw_t;
+    __shared__ __align__(16) float sm_x[NW][L][16][2 * C];  // dl, ds
+    __shared__ __align__(16) float sm_c[NW][L][NP];
+    __shared__ __align__(16) float sm_r[NW][E], sm_p[NW][E];
+    const int item = xcd_item(p.n_items);
+    if (item >= p.n_items) return;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int sg = lane >> 4, cl = lane & 15;
+    const int tile = item % p.tiles;
+    const int g = item / p.tiles % p.G;
+    const int64_t b = item / p.tiles / p.G % (int)p.B;
+    const int seg = item / p.tiles / p.G / (int)p.B + 1;  // nothing needs the first segment's
+    const int ch0 = tile * 16 * C;
+    const int64_t d0 = (int64_t)g * p.per + ch0;
+    const int nch = p.per - ch0 < 16 * C ? p.per - ch0 : 16 * C;
+    const int nv = nch - cl * C < 0 ? 0 : nch - cl * C > C ? C : nch - cl * C;
+    const int64_t len = seq_len(p.lengths, b, p.T);
+    const bool whole = p.vec && nch == 16 * C;
+    float A2[S][C], bias[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int64_t d = d0 + cl * C + c;
+        bias[c] = c < nv && p.delta_bias ? p.delta_bias[d] : 0.f;
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            const int n = sg * S + s;
+            A2[s][c] = c < nv && n < p.N ? p.A[d * p.N + n] * LOG2E : 0.f;
+        }
+    }
+    float edge[FPT], prod[FPT];
+#pragma unroll
+    for (int f = 0; f < FPT; ++f) {
+        edge[f] = 0.f;
+        prod[f] = 1.f;
+    }
+    const uint32_t row = (uint32_t)(p.D * (int64_t)sizeof(T));
+    uint32_t voff[J], coff[BPL];
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+        voff[j] = nv > 0 ? (uint32_t)(4 * j + sg) * row + (uint32_t)(cl * C * sizeof(T)) : NO_CHANNEL;
+    const int64_t row0 = b * p.T * p.D + d0;
+    const int64_t brow = (int64_t)p.G * p.N, b0 = (b * p.T * p.G + g) * p.N;
+#pragma unroll
+    for (int i = 0; i < BPL; ++i) {
+        const int q = lane + 64 * i, t = q / NP, n = q % NP;
+        coff[i] = q < L * NP && n < p.N ? (uint32_t)((t * brow + n) * (int64_t)sizeof(T)) : NO_CHANNEL;
+    }
+    raw_t dr[J], zr[J], gr[J];
+    one_t cr[BPL];
+    const auto load = [&](int64_t t0) {
+        const int64_t left = steps_left<L>(t0, len);
+        load_rows<T, C, J>(make_rows(static_cast<const T *>(p.delta) + row0 + t0 * p.D, left * row), voff, nv, whole,
+                           dr);
+        load_rows<T, C, J>(make_rows(static_cast<const T *>(p.dy) + row0 + t0 * p.D, left * row), voff, nv, whole, gr);
+        if (p.z)
+            load_rows<T, C, J>(make_rows(static_cast<const T *>(p.z) + row0 + t0 * p.D, left * row), voff, nv, whole,
+                               zr);
+        const rsrc_t rc = make_rows(static_cast<const T *>(p.Cm) + b0 + t0 * brow, left * brow * (int64_t)sizeof(T));
+#pragma unroll
+        for (int i = 0; i < BPL; ++i) cr[i] = buf_read<T, 1>(rc, coff[i]);
+    };
+    const int64_t blk0 = seg * (p.seg / (NW * L));
+    const int64_t all = (p.T + NW * L - 1) / (NW * L), end = blk0 + p.seg / (NW * L);
+    const int64_t blk1 = end < all ? end : all;
+    load((blk1 - 1) * (NW * L) + wave * L);
+    for (int64_t blk = blk1 - 1; blk >= blk0; --blk) {
+        const int64_t t0 = blk * (NW * L) + wave * L;
+        const int left = steps_left<L>(t0, len);
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            float dd[C], z[C], gy[C], x[2 * C];
+            PC::unpack(dr[j], dd);
+            PC::unpack(gr[j], gy);
+            if (p.z) PC::unpack(zr[j], z);
+            const bool in = 4 * j + sg < left;
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const float r = gate_rate(dd[c] + bias[c], p.softplus, nullptr);
+                x[c] = in ? r : 0.f;
+                x[C + c] = p.z ? gy[c] * silu(z[c]) : gy[c];
+            }
+            lds_write<2 * C>(sm_x[wave][4 * j + sg][cl], x);
+        }
+#pragma unroll
+        for (int i = 0; i < BPL; ++i) {
+            const int q = lane + 64 * i;
+            if (L * NP % 64 == 0 || q < L * NP) Pack<T, 1>::unpack(cr[i], &sm_c[wave][q / NP][q % NP]);
+        }
+        if (blk > blk0) load(t0 - NW * L);
+        wave_lds_sync();
+        float gv[EL], pv[EL], sum[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) sum[c] = 0.f;
+#pragma unroll
+        for (int t = L - 1; t >= 0; --t) {
+            float x[2 * C], ct[S];
+            lds_read<2 * C>(sm_x[wave][t][cl], x);
+            lds_read<S>(&sm_c[wave][t][sg * S], ct);
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                sum[c] += x[c];
+#pragma unroll
+                for (int s = 0; s < S; ++s)
+                    gv[c * S + s] = __builtin_amdgcn_exp2f(x[c] * A2[s][c]) *
+                                    (t == L - 1 ? ct[s] * x[C + c] : fmaf(ct[s], x[C + c], gv[c * S + s]));
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int s = 0; s < S; ++s) pv[c * S + s] = __builtin_amdgcn_exp2f(sum[c] * A2[s][c]);
+        LV::write(sm_r[wave], lane, gv);
+        LV::write(sm_p[wave], lane, pv);
+        wg_lds_sync();
+#pragma unroll
+        for (int f = 0; f < FPT; ++f) {
+            const int i = tid + f * NT;
+            if (i < E) {
+#pragma unroll
+                for (int w = NW - 1; w >= 0; --w) {
+                    edge[f] = fmaf(sm_p[w][i], edge[f], sm_r[w][i]);
+                    prod[f] *= sm_p[w][i];
+                }
+            }
+        }
+        wg_lds_sync();
+    }
+#pragma unroll
+    for (int f = 0; f < FPT; ++f) {
+        const int i = tid + f * NT;
+        int ln, e;
+        LV::where(i < E ? i : 0, &ln, &e);
+        const int n = (ln >> 4) * S + e % S, ch = (ln & 15) * C + e / S;
+        if (i < E && n < p.N && ch < nch) {
+            const int64_t at = ((seg * p.B + b) * p.D + d0 + ch) * p.N + n;
+            p.seg_v[at] = edge[f];
+            p.seg_p[at] = prod[f];
+        }
+    }
+}
+
 template <typename T, int S, int C, int L, int NW, bool GATED>
 __global__ __launch_bounds__(NW * 64, 2) void scan_bwd_kernel(ScanArgs p) {
     constexpr int EL = S * C, J = L / 4, NP = 4 * S;
@@ -102,7 +254,8 @@ __global__ __launch_bounds__(NW * 64, 2) void scan_bwd_kernel(ScanArgs p) {
     const int sg = lane >> 4, cl = lane & 15;
     const int tile = item % p.tiles;
     const int g = item / p.tiles % p.G;
-    const int64_t b = item / p.tiles / p.G;
+    const int64_t b = item / p.tiles / p.G % (int)p.B;
+    const int seg = item / p.tiles / p.G / (int)p.B;
     const int ch0 = tile * 16 * C;
     const int64_t d0 = (int64_t)g * p.per + ch0;
     const int nch = p.per - ch0 < 16 * C ? p.per - ch0 : 16 * C;
@@ -138,6 +291,12 @@ __global__ __launch_bounds__(NW * 64, 2) void scan_bwd_kernel(ScanArgs p) {
         const int n = (ln >> 4) * S + e % S, ch = (ln & 15) * C + e / S;
         st_off[f] = i < 2 * E && n < p.N && ch < nch ? ch * (int)p.N + n : -1;
         edge[f] = i >= E && st_off[f] >= 0 && p.dhT ? p.dhT[st_base + st_off[f]] : 0.f;
+        if (i >= E && st_off[f] >= 0) {
+            const float *v = p.seg_v + st_base + st_off[f], *q = p.seg_p + st_base + st_off[f];
+#pragma unroll 4
+            for (int k = p.n_seg - 1; k > seg; --k)
+                edge[f] = fmaf(q[k * p.B * p.D * p.N], edge[f], v[k * p.B * p.D * p.N]);
+        }
     }
     const uint32_t row = (uint32_t)(p.D * (int64_t)sizeof(T));
     uint32_t voff[J], boff[BPL];
@@ -181,8 +340,10 @@ __global__ __launch_bounds__(NW * 64, 2) void scan_bwd_kernel(ScanArgs p) {
             if (tid + f * NT < E) edge[f] = st_off[f] >= 0 ? st[st_off[f]] : 0.f;
     };
 
-    if (n_blk > 0) load(n_blk - 1);
-    for (int64_t blk = n_blk - 1; blk >= 0; --blk) {
+    const int64_t blk0 = seg * (p.seg / (NW * L)), end = blk0 + p.seg / (NW * L);
+    const int64_t blk1 = end < n_blk ? end : n_blk;
+    if (blk1 > blk0) load(blk1 - 1);
+    for (int64_t blk = blk1 - 1; blk >= blk0; --blk) {
         const int64_t t0 = blk * (NW * L) + wave * L;
         const int left = steps_left<L>(t0, len), rows = steps_left<L>(t0, p.T);
         {
@@ -402,7 +563,7 @@ __global__ __launch_bounds__(NW * 64, 2) void scan_bwd_kernel(ScanArgs p) {
                 wave_lds_sync();
             }
             if constexpr (t == L / 2) {  // half the gates are done with: registers for the next block's rows
-                if (blk > 0) load(blk - 1);
+                if (blk > blk0) load(blk - 1);
             }
             if constexpr (t % 4 == 0) {  // four steps are complete: their rows
                 constexpr int j = t / 4;
@@ -431,7 +592,7 @@ __global__ __launch_bounds__(NW * 64, 2) void scan_bwd_kernel(ScanArgs p) {
     }
 #pragma unroll
     for (int f = 0; f < FPT; ++f)
-        if (tid + f * NT >= E && st_off[f] >= 0 && p.dh0) p.dh0[st_base + st_off[f]] = edge[f];
+        if (tid + f * NT >= E && st_off[f] >= 0 && p.dh0 && seg == 0) p.dh0[st_base + st_off[f]] = edge[f];
     // dA over the waves; dskip and ddelta_bias over the waves and lane rows too
     float ev[EL], kb[2 * C];
 #pragma unroll
@@ -444,7 +605,7 @@ __global__ __launch_bounds__(NW * 64, 2) void scan_bwd_kernel(ScanArgs p) {
     LV::write(my.r, lane, ev);
     lds_write<2 * C>(my.x[sg][cl], kb);
     wg_lds_sync();
-    float *pa = p.part_a + b * (p.N + 2) * p.D;
+    float *pa = p.part_a + (b * p.n_seg + seg) * (p.N + 2) * p.D;
 #pragma unroll
     for (int f = 0; f < FPT; ++f) {
         const int i = tid + f * NT;
@@ -499,14 +660,32 @@ int64_t bwd_tiles(int64_t per, int64_t N) {
     return (per + w - 1) / w;
 }
 
+// Segments of the backward: none where the channel tiles make 192 workgroups (its
+// LDS holds one a CU), else as many as make 256.
+int64_t bwd_segments(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N) {
+    const int64_t n = B * G * bwd_tiles(D / G, N), blk = scan_block(N), blocks = (T + blk - 1) / blk;
+    if (n >= 192 || blocks < 2) return 1;
+    const int64_t want = (256 + n - 1) / n, seg = (blocks + want - 1) / want;
+    return (blocks + seg - 1) / seg;
+}
+
 template <typename T, int S>
 mi_status launch_bwd(ScanArgs a, hipStream_t s) {
     using TL = BwdTile<S>;
     constexpr int SH = TL::NW * (int)sizeof(BwdWave<S, TL::C, TL::L>);
     static_assert(SH <= 160 * 1024, "a workgroup's LDS");
+    constexpr int64_t BLK = TL::NW * TL::L;
     a.tiles = (int)bwd_tiles(a.per, a.N);
+    a.seg = (a.T + BLK * a.n_seg - 1) / (BLK * a.n_seg) * BLK;
     int64_t items;
-    if (!mul_ok(a.B, a.G, a.tiles, 1, &items) || items > 0x7ffffff0) return MI_ERR_UNSUPPORTED;
+    if (!mul_ok(a.B, a.G, a.tiles, a.n_seg, &items) || items > 0x7ffffff0) return MI_ERR_UNSUPPORTED;
+    if (a.n_seg > 1) {
+        a.n_items = (int)(items / a.n_seg * (a.n_seg - 1));
+        hipLaunchKernelGGL((scan_bwd_sum_kernel<T, S, TL::C, TL::L, TL::NW>), dim3(xcd_grid(a.n_items)),
+                           dim3(TL::NW * 64), 0, s, a);
+        const mi_status st = launch_status();
+        if (st != MI_OK) return st;
+    }
     a.n_items = (int)items;
     const auto kernel = a.z ? scan_bwd_kernel<T, S, TL::C, TL::L, TL::NW, true>
                             : scan_bwd_kernel<T, S, TL::C, TL::L, TL::NW, false>;
@@ -532,15 +711,20 @@ mi_status launch_bwd_t(const ScanArgs &a, void *dBm, void *dCm, hipStream_t s) {
                         StoreShared<T>{static_cast<T *>(dBm), static_cast<T *>(dCm), bc}, s);
 }
 
-// Workspace: partial dBm and dCm, then partial dA, dskip, ddelta_bias.
+// Workspace: partial dBm and dCm; partial dA, dskip, ddelta_bias; the segments'
+// transforms.
 struct BwdWs {
-    int64_t bc, total;
+    int64_t bc, a, n_seg, total;  // bytes, bytes, segments, bytes
 };
 bool bwd_ws(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N, BwdWs *w) {
-    int64_t x, y;
-    if (!mul_ok(B, T, G, N, &x) || !mul_ok(x, bwd_tiles(D / G, N), 8, 1, &x) || !mul_ok(B, N + 2, D, 4, &y)) return false;
+    int64_t x, y, v;
+    w->n_seg = bwd_segments(B, T, D, G, N);
+    if (!mul_ok(B, T, G, N, &x) || !mul_ok(x, bwd_tiles(D / G, N), 8, 1, &x) ||
+        !mul_ok(B * w->n_seg, N + 2, D, 4, &y) || !mul_ok(w->n_seg > 1 ? B * w->n_seg : 0, N, D, 8, &v))
+        return false;
     w->bc = (int64_t)round_up((size_t)x, 256);
-    return !__builtin_add_overflow(w->bc, y, &w->total);
+    w->a = (int64_t)round_up((size_t)y, 256);
+    return !__builtin_add_overflow(w->bc, w->a, &w->total) && !__builtin_add_overflow(w->total, v, &w->total);
 }
 
 }  // namespace
@@ -593,12 +777,15 @@ mi_status mi_selective_scan_bwd(const void *u, const void *delta, const float *A
         if ((st = check_ws_lists(ws, ws_bytes, (size_t)w.total, in, out)) != MI_OK) return st;
         a.part_bc = static_cast<float *>(ws);
         a.part_a = reinterpret_cast<float *>(static_cast<char *>(ws) + w.bc);
+        a.n_seg = (int)w.n_seg;
+        a.seg_v = reinterpret_cast<float *>(static_cast<char *>(ws) + w.bc + w.a);
+        a.seg_p = a.seg_v + w.n_seg * B * D * N;
         if (dt == MI_F32) st = launch_bwd_t<float>(a, dBm, dCm, stream);
         else if (dt == MI_BF16) st = launch_bwd_t<bf16_t>(a, dBm, dCm, stream);
         else st = launch_bwd_t<f16_t>(a, dBm, dCm, stream);
         if (st != MI_OK) return st;
     }
-    return reduce_parts(a.part_a, B, (N + 2) * D, StoreParams{dA, dskip, ddelta_bias, D, N}, stream);
+    return reduce_parts(a.part_a, B * (B > 0 ? a.n_seg : 1), (N + 2) * D, StoreParams{dA, dskip, ddelta_bias, D, N}, stream);
 }
 
 }  // extern "C"

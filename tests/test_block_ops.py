@@ -205,8 +205,9 @@ def test_scan_refusals():
     (u, delta, A, Bm, Cm, skip, z, db, h0, ln, y, hT, st, dy, dhT, du, dd, dA, dB, dC, dsk, dz, ddb, dh0,
      ws) = ptrs(25)
 
-    def fwd(u=u, delta=delta, A=A, Bm=Bm, Cm=Cm, y=y, hT=hT, st=st, sz=(2, 8, 16, 2, 4), dt=0, h0=h0):
-        return L.mi_selective_scan_fwd(u, delta, A, Bm, Cm, skip, z, db, h0, ln, y, hT, st, *sz, 1, dt, None)
+    def fwd(u=u, delta=delta, A=A, Bm=Bm, Cm=Cm, y=y, hT=hT, st=st, sz=(2, 8, 16, 2, 4), dt=0, h0=h0,
+            wsp=ws, wsb=BIG):
+        return L.mi_selective_scan_fwd(u, delta, A, Bm, Cm, skip, z, db, h0, ln, y, hT, st, *sz, 1, dt, wsp, wsb, None)
 
     assert fwd(sz=(2, 8, 16, 2, 0)) == MI_ERR_UNSUPPORTED
     assert fwd(sz=(2, 8, 16, 2, 65)) == MI_ERR_UNSUPPORTED
@@ -222,6 +223,13 @@ def test_scan_refusals():
     assert fwd(y=z) == MI_ERR_INVALID_ARG
     assert fwd(sz=(0, 8, 16, 2, 4), u=None, y=None) == MI_OK
     assert fwd(sz=(1 << 40, 1 << 20, 1 << 10, 1, 4)) == MI_ERR_INVALID_ARG
+    long = (1, 4096, 16, 1, 16)  # one channel tile: segments of the sequence
+    need = L.mi_selective_scan_fwd_workspace(*long, 0)
+    assert need > 0
+    assert fwd(sz=long, wsp=None) == MI_ERR_WORKSPACE
+    assert fwd(sz=long, wsb=need - 1) == MI_ERR_WORKSPACE
+    assert fwd(sz=long, wsp=u) == MI_ERR_INVALID_ARG
+    assert fwd(sz=long, wsp=ws + 4) == MI_ERR_INVALID_ARG
     for N in range(1, 65):
         assert L.mi_selective_scan_block(N) > 0
     assert L.mi_selective_scan_block(0) == 0 and L.mi_selective_scan_block(65) == 0
