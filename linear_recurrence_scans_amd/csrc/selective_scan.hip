@@ -38,17 +38,16 @@ __global__ __launch_bounds__(NW * 64, WPS) void scan_fwd_kernel(ScanArgs p) {
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int sg = lane >> 4, cl = lane & 15;
-    const int tile = item % p.tiles;
-    const int g = item / p.tiles % p.G;
-    const int64_t b = item / p.tiles / p.G % (int)p.B;
-    const int seg = item / p.tiles / p.G / (int)p.B;
+    const Item it(item, p);
+    const int tile = it.tile, g = it.g, seg = it.seg;
+    const int64_t b = it.b;
     const int64_t t_first = seg * p.seg, t_last = t_first + p.seg < p.T ? t_first + p.seg : p.T;
     const int ch0 = tile * 16 * C;                  // first channel of the tile inside its group
     const int64_t d0 = (int64_t)g * p.per + ch0;
     const int nch = p.per - ch0 < 16 * C ? p.per - ch0 : 16 * C;
     const int nv = nch - cl * C < 0 ? 0 : nch - cl * C > C ? C : nch - cl * C;
     const int64_t len = seq_len(p.lengths, b, p.T);
-    const bool whole = p.vec && nch == 16 * C;      // every lane reads and writes whole vectors
+    const bool whole = C == 1 || p.vec;             // rows go by whole vectors
     float A2[S][C], skip[C], bias[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -116,8 +115,11 @@ __global__ __launch_bounds__(NW * 64, WPS) void scan_fwd_kernel(ScanArgs p) {
         }
     };
 
+    // blocks past the sequence's end leave the state and have zero rows
+    const int64_t t_end = len < t_last ? (len < t_first ? t_first : (len - t_first + NW * L - 1) / (NW * L) * (NW * L) + t_first)
+                                       : t_last;
     load(t_first + wave * L);
-    for (int64_t tb = t_first; tb < t_last; tb += NW * L) {
+    for (int64_t tb = t_first; tb < t_end; tb += NW * L) {
         const int64_t t0 = tb + wave * L;
         const int left = steps_left<L>(t0, len);
         // this wave's rows: dl and dl u by the lanes that own them
@@ -147,7 +149,7 @@ __global__ __launch_bounds__(NW * 64, WPS) void scan_fwd_kernel(ScanArgs p) {
                 if (!SUM) Pack<T, 1>::unpack(cr[i], &sm_c[wave][t][n]);
             }
         }
-        if (tb + NW * L < t_last) load(t0 + NW * L);
+        if (tb + NW * L < t_end) load(t0 + NW * L);
         wave_lds_sync();
         // the wave's steps from a zero state
         float a[L][S][C], h[S][C], yl[L][C], sum[C];
@@ -281,6 +283,23 @@ __global__ __launch_bounds__(NW * 64, WPS) void scan_fwd_kernel(ScanArgs p) {
                 p.seg_p[at] = prod[f];
             }
         return;
+    }
+    const float zero[C] = {};
+    for (int64_t tb = t_end; tb < t_last; tb += NW * L) {
+        const int64_t t0 = tb + wave * L;
+        char *y = reinterpret_cast<char *>(static_cast<T *>(p.y) + row0 + t0 * p.D);
+        const int rows = steps_left<L>(t0, p.T);
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+            if (4 * j + sg < rows) store_ch<T, C>(y + voff[j], nv, whole, zero);
+    }
+    if (p.states) {
+        constexpr int64_t BLK = scan_block_of<S>();
+        const int64_t n_blk = (p.T + BLK - 1) / BLK;
+        for (int64_t k = (t_end + BLK - 1) / BLK; k * BLK < t_last; ++k)
+#pragma unroll
+            for (int f = 0; f < FPT; ++f)
+                if (st_off[f] >= 0) p.states[(b * n_blk + k) * p.D * p.N + d0 * p.N + st_off[f]] = carry[f];
     }
     if (p.hT && seg == p.n_seg - 1)
 #pragma unroll

@@ -48,7 +48,7 @@ struct ScanArgs {
     float *seg_v, *seg_p;  // (n_seg, B, D, N) transform of a segment: its scan from zero, its gates' product
     int n_items;           // n_seg * B * G * tiles
     int softplus;
-    int vec;               // rows may be read C channels at a time
+    int vec;               // rows may be read two channels at a time: no tile ends inside a pair
 };
 
 // Tiles by S, the states a lane holds: C channels a lane, L steps a wave, NW waves
@@ -97,6 +97,17 @@ __device__ __forceinline__ int xcd_item(int n) {
     const int per = (n + 7) / 8;
     return (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
 }
+// Sequences vary fastest, so that short and long ones spread over the XCDs.
+struct Item {
+    int b, tile, g, seg;
+    __device__ __forceinline__ Item(int item, const ScanArgs &p) {
+        const int nb = (int)p.B;
+        b = item % nb;
+        tile = item / nb % p.tiles;
+        g = item / nb / p.tiles % p.G;
+        seg = item / nb / p.tiles / p.G;
+    }
+};
 inline unsigned xcd_grid(int n) { return (unsigned)((n + 7) / 8 * 8); }
 
 // Row-joined sums: y[t][c] holds this lane's part for steps t = 4 j + i; on
@@ -140,8 +151,8 @@ __device__ __forceinline__ typename Pack<T, N>::raw_t buf_read(rsrc_t r, uint32_
     else return __builtin_bit_cast(raw_t, __builtin_amdgcn_raw_buffer_load_b16(r, voff, 0, 0));
 }
 
-// The C channels of J rows at offsets voff: whole vectors, or single elements
-// of which the first nv exist.
+// The C channels of J rows at offsets voff: whole vectors (a lane then has C
+// channels or none), or single elements of which the first nv exist.
 template <typename T, int C, int J>
 __device__ __forceinline__ void load_rows(rsrc_t r, const uint32_t (&voff)[J], int nv, bool whole,
                                           typename Pack<T, C>::raw_t (&raw)[J]) {
@@ -164,7 +175,7 @@ __device__ __forceinline__ void load_rows(rsrc_t r, const uint32_t (&voff)[J], i
 template <typename T, int C>
 __device__ __forceinline__ void store_ch(char *p, int nv, bool whole, const float (&f)[C]) {
     if (whole) {
-        *reinterpret_cast<typename Pack<T, C>::raw_t *>(p) = Pack<T, C>::pack(f);
+        if (nv > 0) *reinterpret_cast<typename Pack<T, C>::raw_t *>(p) = Pack<T, C>::pack(f);
     } else {
 #pragma unroll
         for (int c = 0; c < C; ++c)

@@ -97,16 +97,15 @@ __global__ __launch_bounds__(NW * 64) void scan_bwd_sum_kernel(ScanArgs p) {
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int sg = lane >> 4, cl = lane & 15;
-    const int tile = item % p.tiles;
-    const int g = item / p.tiles % p.G;
-    const int64_t b = item / p.tiles / p.G % (int)p.B;
-    const int seg = item / p.tiles / p.G / (int)p.B + 1;  // nothing needs the first segment's
+    const Item it(item, p);
+    const int tile = it.tile, g = it.g, seg = it.seg + 1;  // nothing needs the first segment's
+    const int64_t b = it.b;
     const int ch0 = tile * 16 * C;
     const int64_t d0 = (int64_t)g * p.per + ch0;
     const int nch = p.per - ch0 < 16 * C ? p.per - ch0 : 16 * C;
     const int nv = nch - cl * C < 0 ? 0 : nch - cl * C > C ? C : nch - cl * C;
     const int64_t len = seq_len(p.lengths, b, p.T);
-    const bool whole = p.vec && nch == 16 * C;
+    const bool whole = C == 1 || p.vec;
     float A2[S][C], bias[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -151,9 +150,10 @@ __global__ __launch_bounds__(NW * 64) void scan_bwd_sum_kernel(ScanArgs p) {
         for (int i = 0; i < BPL; ++i) cr[i] = buf_read<T, 1>(rc, coff[i]);
     };
     const int64_t blk0 = seg * (p.seg / (NW * L));
-    const int64_t all = (p.T + NW * L - 1) / (NW * L), end = blk0 + p.seg / (NW * L);
-    const int64_t blk1 = end < all ? end : all;
-    load((blk1 - 1) * (NW * L) + wave * L);
+    const int64_t end = blk0 + p.seg / (NW * L);
+    // blocks past the sequence's end pass the gradient on
+    const int64_t live = (len + NW * L - 1) / (NW * L), blk1 = end < live ? end : live;
+    if (blk1 > blk0) load((blk1 - 1) * (NW * L) + wave * L);
     for (int64_t blk = blk1 - 1; blk >= blk0; --blk) {
         const int64_t t0 = blk * (NW * L) + wave * L;
         const int left = steps_left<L>(t0, len);
@@ -252,16 +252,15 @@ __global__ __launch_bounds__(NW * 64, 2) void scan_bwd_kernel(ScanArgs p) {
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     W &my = sm[wave];
     const int sg = lane >> 4, cl = lane & 15;
-    const int tile = item % p.tiles;
-    const int g = item / p.tiles % p.G;
-    const int64_t b = item / p.tiles / p.G % (int)p.B;
-    const int seg = item / p.tiles / p.G / (int)p.B;
+    const Item it(item, p);
+    const int tile = it.tile, g = it.g, seg = it.seg;
+    const int64_t b = it.b;
     const int ch0 = tile * 16 * C;
     const int64_t d0 = (int64_t)g * p.per + ch0;
     const int nch = p.per - ch0 < 16 * C ? p.per - ch0 : 16 * C;
     const int nv = nch - cl * C < 0 ? 0 : nch - cl * C > C ? C : nch - cl * C;
     const int64_t len = seq_len(p.lengths, b, p.T);
-    const bool whole = p.vec && nch == 16 * C;
+    const bool whole = C == 1 || p.vec;
     float A2[S][C], skip[C], bias[C], dA[S][C], dskip[C], dbias[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -341,7 +340,28 @@ __global__ __launch_bounds__(NW * 64, 2) void scan_bwd_kernel(ScanArgs p) {
     };
 
     const int64_t blk0 = seg * (p.seg / (NW * L)), end = blk0 + p.seg / (NW * L);
-    const int64_t blk1 = end < n_blk ? end : n_blk;
+    // blocks past the sequence's end pass the gradient on and have zero rows
+    const int64_t last = end < n_blk ? end : n_blk, live = (len + NW * L - 1) / (NW * L);
+    const int64_t blk1 = last < live ? last : live > blk0 ? live : blk0;
+    for (int64_t blk = blk1; blk < last; ++blk) {
+        const int64_t t0 = blk * (NW * L) + wave * L;
+        const int rows = steps_left<L>(t0, p.T);
+        const float zero[C] = {};
+        const int64_t at = row0 + t0 * p.D;
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+            if (4 * j + sg < rows) {
+                store_ch<T, C>(reinterpret_cast<char *>(static_cast<T *>(p.du) + at) + voff[j], nv, whole, zero);
+                store_ch<T, C>(reinterpret_cast<char *>(static_cast<T *>(p.ddelta) + at) + voff[j], nv, whole, zero);
+                if constexpr (GATED)
+                    store_ch<T, C>(reinterpret_cast<char *>(static_cast<T *>(p.dz) + at) + voff[j], nv, whole, zero);
+            }
+        for (int q = lane; q < L * NP; q += 64)
+            if (q / NP < rows && q % NP < p.N) {
+                part_b[(t0 + q / NP) * brow + q % NP] = 0.f;
+                part_c[(t0 + q / NP) * brow + q % NP] = 0.f;
+            }
+    }
     if (blk1 > blk0) load(blk1 - 1);
     for (int64_t blk = blk1 - 1; blk >= blk0; --blk) {
         const int64_t t0 = blk * (NW * L) + wave * L;
