@@ -414,17 +414,18 @@ mi_status launch_tile(ScanArgs a, int64_t n_seg, hipStream_t s) {
 }
 
 // How a call is cut, by the number of workgroups that its channel tiles make.
-//  - 768 or more (three a CU): workgroups of 4 waves at 3 waves a SIMD, which
+//  - 640 or more wide tiles: workgroups of 4 waves at 3 waves a SIMD, which
 //    overlap each other's folds; B = 8, T = 4096, D = 4096, N = 16, bf16 (1024):
-//    744 us, against 892 with 8 waves.
-//  - fewer: 8 waves, so that a workgroup a CU still fills half of it; B = 2, T =
-//    4096, D = 4096 with z (256): 225 us, against 349 with 4 waves.
-//  - fewer than 256: narrow tiles (one channel a lane) of 16 waves, while those
-//    make at least 192 workgroups: four times the waves; B = 1, T = 8192, D = 4096
-//    with z (128 wide, 256 narrow): 245 us, against 456 with wide tiles of 8 waves.
+//    744 us, against 892 with 8 waves.  At B = 5, T = 2048 (640) wide tiles of 8
+//    waves and narrow ones take the same, 335 and 339 us.
+//  - fewer: narrow tiles (one channel a lane) of 16 waves, while those make at
+//    least 192 workgroups: twice the workgroups, four times the waves; B = 3, T =
+//    4096, D = 4096 with z (384 wide): 300 us against 445 with wide tiles of 8
+//    waves, B = 4, T = 4096, D = 2048 (256 wide): 196 against 226.  (N > 32, whose
+//    tiles are narrow already and whose LDS holds 8 waves: 8 waves.)
 //  - fewer still: segments of the sequence, as many as make 768 workgroups of 4
-//    waves.
-enum FwdCut { FWD_MANY, FWD_EIGHT, FWD_NARROW, FWD_SEGMENTS };
+//    waves; B = 1, T = 4096, D = 2048 (64 wide): 102 us, against 121 narrow.
+enum FwdCut { FWD_MANY, FWD_NARROW, FWD_SEGMENTS };
 struct FwdPlan {
     FwdCut cut;
     int64_t n_seg;
@@ -433,9 +434,8 @@ template <int S>
 FwdPlan fwd_plan(int64_t B, int64_t G, int64_t per, int64_t T) {
     constexpr int C = FwdTile<S>::C, L = FwdTile<S>::L;
     const int64_t n = B * G * ((per + 16 * C - 1) / (16 * C)), narrow = B * G * ((per + 15) / 16);
-    if (n >= 768) return {FWD_MANY, 1};
-    if (n >= 256) return {FWD_EIGHT, 1};
-    if (S < 16 && narrow >= 192) return {FWD_NARROW, 1};
+    if (n >= 640) return {FWD_MANY, 1};
+    if (narrow >= 192) return {FWD_NARROW, 1};
     const int64_t blocks = (T + 4 * L - 1) / (4 * L), want = (768 + n - 1) / n;
     const int64_t seg = (blocks + want - 1) / want;  // blocks a segment
     return {FWD_SEGMENTS, blocks < 2 || seg < 1 ? 1 : (blocks + seg - 1) / seg};
@@ -456,9 +456,7 @@ mi_status launch_fwd(const ScanArgs &a, hipStream_t s) {
     constexpr int WPS = S == 16 ? 2 : 3;
     constexpr int LN = S >= 8 ? 4 : S >= 2 ? 8 : 16;  // narrow: at most 32 gates a lane, 128 registers
     const FwdPlan q = fwd_plan<S>(a.B, a.G, a.per, a.T);
-    if (q.cut == FWD_EIGHT) return launch_tile<T, S, C, L, 8, 2, false>(a, 1, s);
-    if constexpr (S < 16)
-        if (q.cut == FWD_NARROW) return launch_tile<T, S, 1, LN, 16, 4, false>(a, 1, s);
+    if (q.cut == FWD_NARROW) return launch_tile<T, S, 1, LN, S == 16 ? 8 : 16, S == 16 ? 2 : 4, false>(a, 1, s);
     return launch_tile<T, S, C, L, 4, WPS, true>(a, q.n_seg, s);
 }
 template <typename T>
