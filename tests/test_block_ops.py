@@ -725,3 +725,39 @@ def test_offsets_past_32_bits():
         assert bool(torch.isfinite(p).all())
         lim = 2 * R.half_step(t) * p.abs() + 2 * 120 * 2.0 ** -24 * float(p.abs().max())
         assert bool(((p - q).abs() <= lim).all())
+
+
+# ---------------------------------------------------------------------------
+# GPU: every way a scan is cut over workgroups, and the operators together
+# ---------------------------------------------------------------------------
+
+@gpu
+@pytest.mark.parametrize("B,T,D,G,N,lengths", [
+    (1, 1000, 16, 1, 16, None),            # segments of the sequence
+    (2, 700, 24, 1, 4, [700, 333]),        # ... that end inside one, or before it
+    (1, 650, 40, 2, 6, None),
+    (2, 500, 20, 1, 40, [0, 257]),
+    (1, 300, 33, 1, 64, None),
+    (4, 70, 800, 1, 16, [70, 1, 0, 65]),   # narrow tiles
+    (5, 150, 650, 1, 20, None),
+    (16, 40, 1280, 1, 16, None),           # wide tiles, no segments in the backward
+])
+def test_scan_cuts(B, T, D, G, N, lengths):
+    check_scan(B, T, D, G, N, F32, T + D, lengths=lengths)
+
+
+@gpu
+def test_example_trains_and_serves():
+    """The example block: training lowers the loss, steps equal one pass.
+
+    Logits are fp32 sums over the blocks' outputs, of order 1 to 10, through 13
+    operators a block and layer; 1e-3 is 10^3 roundings of the largest."""
+    say("examples/sequence_block.py")
+    import os
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import sequence_block as ex
+    torch.manual_seed(0)
+    model = ex.Model().cuda()
+    losses = ex.train(model, 60)
+    assert losses[-1] < 0.7 * losses[0], (losses[0], losses[-1])
+    assert ex.serve(model, [40, 17, 0, 33], 12) < 1e-3
