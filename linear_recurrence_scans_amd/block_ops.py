@@ -33,6 +33,7 @@ class _Here:
     """Call on the current stream of the current device."""
 
     __slots__ = ("handle",)
+    side = False
 
     def __init__(self, handle):
         self.handle = handle
@@ -42,9 +43,6 @@ class _Here:
 
     def __exit__(self, *exc):
         return False
-
-    def keep(self, *ts):
-        pass
 
 
 # (tensors on a GPU have initialised torch's runtime, so the raw lookups are safe)
@@ -67,13 +65,15 @@ def _act(act) -> int:
 
 
 def _dev_tensor(t, name: str) -> torch.Tensor:
-    _device(t, name)
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        _device(t, name)
     return t if t.is_contiguous() else t.contiguous()
 
 
 def _need(t, like: torch.Tensor, shape, name: str, dtype=None):
     """An input of the given shape on `like`'s device (dtype: `like`'s by default)."""
-    _device(t, name)
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        _device(t, name)
     if t.shape != shape or t.dtype != (dtype or like.dtype) or t.device != like.device:
         raise ValueError("%s must be a %s tensor of shape %s on %s"
                          % (name, dtype or like.dtype, tuple(shape), like.device))
@@ -127,14 +127,16 @@ def mi_causal_conv_fwd(x, w, bias=None, x0=None, *, act=None, lengths=None, y=No
         x, w = _dev_tensor(x, "x"), _dev_tensor(w, "w")
         K = _conv_shape(x, w, 3)
         Bn, T, D = x.shape
-        bias = _opt(bias, x, (D,), "bias", _F32)
-        x0 = _opt(x0, x, (Bn, K - 1, D), "x0")
-        lengths = _opt(lengths, x, (Bn,), "lengths", _I32)
+        bias = None if bias is None else _need(bias, x, (D,), "bias", _F32)
+        x0 = None if x0 is None else _need(x0, x, (Bn, K - 1, D), "x0")
+        lengths = None if lengths is None else _need(lengths, x, (Bn,), "lengths", _I32)
         y, xT = _out(y, x, "y"), _new(xT, x, (Bn, max(K - 1, 0), D), "xT")
-        c.keep(x, w, bias, x0, lengths, y, xT)
+        if c.side:
+            c.keep(x, w, bias, x0, lengths, y, xT)
         st = _load().mi_causal_conv_fwd(x.data_ptr(), w.data_ptr(), _ptr(bias), _ptr(x0), _ptr(lengths),
                                         y.data_ptr(), xT.data_ptr(), Bn, T, D, K, _act(act), _dt(x), c.handle)
-        _check(st, "mi_causal_conv_fwd")
+        if st:
+            _check(st, "mi_causal_conv_fwd")
     return y, xT
 
 
@@ -152,20 +154,22 @@ def mi_causal_conv_bwd(x, w, bias, x0, dy, dxT=None, *, act=None, lengths=None, 
         K = _conv_shape(x, w, 3)
         Bn, T, D = x.shape
         dy = _need(dy, x, x.shape, "dy")
-        bias = _opt(bias, x, (D,), "bias", _F32)
-        x0 = _opt(x0, x, (Bn, K - 1, D), "x0")
-        dxT = _opt(dxT, x, (Bn, K - 1, D), "dxT")
-        lengths = _opt(lengths, x, (Bn,), "lengths", _I32)
+        bias = None if bias is None else _need(bias, x, (D,), "bias", _F32)
+        x0 = None if x0 is None else _need(x0, x, (Bn, K - 1, D), "x0")
+        dxT = None if dxT is None else _need(dxT, x, (Bn, K - 1, D), "dxT")
+        lengths = None if lengths is None else _need(lengths, x, (Bn,), "lengths", _I32)
         dx, dw = _out(dx, x, "dx"), _out(dw, w, "dw")
         dbias = _out(dbias, bias, "dbias") if bias is not None else None
         dx0 = _out(dx0, x0, "dx0") if x0 is not None else None
         dt = _dt(x)
         ws = _workspace(ws, _load().mi_causal_conv_bwd_workspace(Bn, T, D, K, dt), x.device)
-        c.keep(x, w, bias, x0, lengths, dy, dxT, dx, dw, dbias, dx0, ws)
+        if c.side:
+            c.keep(x, w, bias, x0, lengths, dy, dxT, dx, dw, dbias, dx0, ws)
         st = _load().mi_causal_conv_bwd(x.data_ptr(), w.data_ptr(), _ptr(bias), _ptr(x0), _ptr(lengths),
                                         dy.data_ptr(), _ptr(dxT), dx.data_ptr(), dw.data_ptr(), _ptr(dbias),
                                         _ptr(dx0), Bn, T, D, K, _act(act), dt, ws.data_ptr(), _nbytes(ws), c.handle)
-        _check(st, "mi_causal_conv_bwd")
+        if st:
+            _check(st, "mi_causal_conv_bwd")
     return dx, dw, dbias, dx0
 
 
@@ -176,16 +180,18 @@ def mi_causal_conv_step(x, w, bias, x0, *, act=None, y=None, x_out=None, stream=
         x, w = _dev_tensor(x, "x"), _dev_tensor(w, "w")
         K = _conv_shape(x, w, 2)
         Bn, D = x.shape
-        bias = _opt(bias, x, (D,), "bias", _F32)
+        bias = None if bias is None else _need(bias, x, (D,), "bias", _F32)
         own = x0
         x0 = _need(x0, x, (Bn, K - 1, D), "x0")
         if x_out is own and x0 is not own:
             raise ValueError("x0 must be contiguous to be updated in place")
         y, x_out = _out(y, x, "y"), _out(x_out, x0, "x_out")
-        c.keep(x, w, bias, x0, y, x_out)
+        if c.side:
+            c.keep(x, w, bias, x0, y, x_out)
         st = _load().mi_causal_conv_step(x.data_ptr(), w.data_ptr(), _ptr(bias), x0.data_ptr(), y.data_ptr(),
                                          x_out.data_ptr(), Bn, D, K, _act(act), _dt(x), c.handle)
-        _check(st, "mi_causal_conv_step")
+        if st:
+            _check(st, "mi_causal_conv_step")
     return y, x_out
 
 
@@ -217,7 +223,7 @@ def _scan_args(u, delta, A, Bm, Cm, skip, z, delta_bias, dims):
     if Bm.dtype != u.dtype or Bm.device != u.device:
         raise ValueError("u, delta, Bm, Cm and z must share device and dtype (%s, %s)" % (u.device, u.dtype))
     skip, delta_bias = _opt(skip, u, (D,), "skip", _F32), _opt(delta_bias, u, (D,), "delta_bias", _F32)
-    z = _opt(z, u, u.shape, "z")
+    z = None if z is None else _need(z, u, u.shape, "z")
     T = u.shape[1] if dims == 3 else 1
     return (u, delta, A, Bm, Cm, skip, z, delta_bias), (u.shape[0], T, D, G, N)
 
@@ -236,19 +242,21 @@ def mi_selective_scan_fwd(u, delta, A, Bm, Cm, skip=None, z=None, delta_bias=Non
     with _call(stream, _device(u, "u")) as c:
         args, (Bn, T, D, G, N) = _scan_args(u, delta, A, Bm, Cm, skip, z, delta_bias, 3)
         u = args[0]
-        h0 = _opt(h0, u, (Bn, D, N), "h0", _F32)
-        lengths = _opt(lengths, u, (Bn,), "lengths", _I32)
+        h0 = None if h0 is None else _need(h0, u, (Bn, D, N), "h0", _F32)
+        lengths = None if lengths is None else _need(lengths, u, (Bn,), "lengths", _I32)
         y, hT = _out(y, u, "y"), _new(hT, u, (Bn, D, N), "hT", _F32)
         if save_states or states is not None:
             blk = max(1, mi_selective_scan_block(N))
             states = _new(states, u, (Bn, (T + blk - 1) // blk, D, N), "states", _F32)
         lib, dt = _load(), _dt(u)
         ws = _workspace(ws, lib.mi_selective_scan_fwd_workspace(Bn, T, D, G, N, dt), u.device)
-        c.keep(*args, h0, lengths, y, hT, states, ws)
+        if c.side:
+            c.keep(*args, h0, lengths, y, hT, states, ws)
         st = lib.mi_selective_scan_fwd(*(_ptr(t) for t in args), _ptr(h0), _ptr(lengths), y.data_ptr(),
                                        hT.data_ptr(), _ptr(states), Bn, T, D, G, N, int(bool(softplus)), dt,
                                        ws.data_ptr(), _nbytes(ws), c.handle)
-        _check(st, "mi_selective_scan_fwd")
+        if st:
+            _check(st, "mi_selective_scan_fwd")
     return y, hT, states
 
 
@@ -268,21 +276,23 @@ def mi_selective_scan_bwd(u, delta, A, Bm, Cm, states, dy, dhT=None, skip=None, 
         blk = max(1, mi_selective_scan_block(N))
         states = _need(states, u, (Bn, (T + blk - 1) // blk, D, N), "states", _F32)
         dy = _need(dy, u, u.shape, "dy")
-        dhT = _opt(dhT, u, (Bn, D, N), "dhT", _F32)
-        h0 = _opt(h0, u, (Bn, D, N), "h0", _F32)
-        lengths = _opt(lengths, u, (Bn,), "lengths", _I32)
+        dhT = None if dhT is None else _need(dhT, u, (Bn, D, N), "dhT", _F32)
+        h0 = None if h0 is None else _need(h0, u, (Bn, D, N), "h0", _F32)
+        lengths = None if lengths is None else _need(lengths, u, (Bn,), "lengths", _I32)
         grads = [torch.empty_like(t) if t is not None else None
                  for t in (u, delta, A, Bm, Cm, skip, z, delta_bias, h0)]
         du, ddelta, dA, dBm, dCm, dskip, dz, dbias, dh0 = grads
         dt = _dt(u)
         ws = _workspace(ws, _load().mi_selective_scan_bwd_workspace(Bn, T, D, G, N, dt), u.device)
-        c.keep(*args, states, dy, dhT, lengths, *grads, ws)
+        if c.side:
+            c.keep(*args, states, dy, dhT, lengths, *grads, ws)
         st = _load().mi_selective_scan_bwd(*(_ptr(t) for t in args), states.data_ptr(), _ptr(lengths), dy.data_ptr(),
                                            _ptr(dhT), du.data_ptr(), ddelta.data_ptr(), dA.data_ptr(),
                                            dBm.data_ptr(), dCm.data_ptr(), _ptr(dskip), _ptr(dz), _ptr(dbias),
                                            _ptr(dh0), Bn, T, D, G, N, int(bool(softplus)), dt, ws.data_ptr(),
                                            _nbytes(ws), c.handle)
-        _check(st, "mi_selective_scan_bwd")
+        if st:
+            _check(st, "mi_selective_scan_bwd")
     return tuple(grads)
 
 
@@ -299,12 +309,14 @@ def mi_selective_scan_step(u, delta, A, Bm, Cm, h, skip=None, z=None, delta_bias
         if h_out is own and h is not own:
             raise ValueError("h must be contiguous to be updated in place")
         y, h_out = _out(y, u, "y"), _out(h_out, h, "h_out")
-        c.keep(*args, h, y, h_out)
+        if c.side:
+            c.keep(*args, h, y, h_out)
         st = _load().mi_selective_scan_step(u.data_ptr(), delta.data_ptr(), A.data_ptr(), Bm.data_ptr(),
                                             Cm.data_ptr(), h.data_ptr(), _ptr(skip), _ptr(z), _ptr(delta_bias),
                                             y.data_ptr(), h_out.data_ptr(), Bn, D, G, N, int(bool(softplus)),
                                             _dt(u), c.handle)
-        _check(st, "mi_selective_scan_step")
+        if st:
+            _check(st, "mi_selective_scan_step")
     return y, h_out
 
 
@@ -322,7 +334,7 @@ def _norm_args(x, w, bias, z, groups, act):
     if z is not None and act is not None:
         raise ValueError("act and z exclude each other")
     w, bias = _opt(w, x, (D,), "w", _F32), _opt(bias, x, (D,), "bias", _F32)
-    z = _opt(z, x, x.shape, "z")
+    z = None if z is None else _need(z, x, x.shape, "z")
     rows = 1
     for n in x.shape[:-1]:
         rows *= n
@@ -337,10 +349,12 @@ def mi_group_norm_fwd(x, w=None, bias=None, z=None, *, groups=1, eps=1e-5, cente
     with _call(stream, _device(x, "x")) as c:
         x, w, bias, z, R, D = _norm_args(x, w, bias, z, groups, act)
         y = _out(y, x, "y")
-        c.keep(x, w, bias, z, y)
+        if c.side:
+            c.keep(x, w, bias, z, y)
         st = _load().mi_group_norm_fwd(x.data_ptr(), _ptr(w), _ptr(bias), _ptr(z), y.data_ptr(), R, D, groups, eps,
                                        int(bool(centered)), _act(act), _dt(x), c.handle)
-        _check(st, "mi_group_norm_fwd")
+        if st:
+            _check(st, "mi_group_norm_fwd")
     return y
 
 
@@ -360,9 +374,11 @@ def mi_group_norm_bwd(x, w, bias, dy, z=None, *, groups=1, eps=1e-5, centered=Tr
         dw, dbias, dz = (torch.empty_like(t) if t is not None else None for t in (w, bias, z))
         dt = _dt(x)
         ws = _workspace(ws, _load().mi_group_norm_bwd_workspace(R, D, groups, dt), x.device)
-        c.keep(x, w, bias, z, dy, dx, dw, dbias, dz, ws)
+        if c.side:
+            c.keep(x, w, bias, z, dy, dx, dw, dbias, dz, ws)
         st = _load().mi_group_norm_bwd(x.data_ptr(), _ptr(w), _ptr(bias), _ptr(z), dy.data_ptr(), dx.data_ptr(),
                                        _ptr(dw), _ptr(dbias), _ptr(dz), R, D, groups, eps, int(bool(centered)),
                                        _act(act), dt, ws.data_ptr(), _nbytes(ws), c.handle)
-        _check(st, "mi_group_norm_bwd")
+        if st:
+            _check(st, "mi_group_norm_bwd")
     return dx, dw, dbias, dz
