@@ -17,8 +17,8 @@ from . import _Call, _check, _device, _dt, _load, _workspace
 
 __all__ = [
     "mi_causal_conv_fwd", "mi_causal_conv_bwd", "mi_causal_conv_bwd_workspace", "mi_causal_conv_step",
-    "mi_selective_scan_block", "mi_selective_scan_fwd_workspace", "mi_selective_scan_fwd", "mi_selective_scan_bwd", "mi_selective_scan_bwd_workspace",
-    "mi_selective_scan_step",
+    "mi_selective_scan_block", "mi_selective_scan_fwd", "mi_selective_scan_fwd_workspace", "mi_selective_scan_bwd",
+    "mi_selective_scan_bwd_workspace", "mi_selective_scan_step",
     "mi_group_norm_fwd", "mi_group_norm_bwd", "mi_group_norm_bwd_workspace",
 ]
 
@@ -249,12 +249,14 @@ def mi_selective_scan_fwd(u, delta, A, Bm, Cm, skip=None, z=None, delta_bias=Non
             blk = max(1, mi_selective_scan_block(N))
             states = _new(states, u, (Bn, (T + blk - 1) // blk, D, N), "states", _F32)
         lib, dt = _load(), _dt(u)
-        ws = _workspace(ws, lib.mi_selective_scan_fwd_workspace(Bn, T, D, G, N, dt), u.device)
+        need = lib.mi_selective_scan_fwd_workspace(Bn, T, D, G, N, dt)
+        if need:
+            ws = _workspace(ws, need, u.device)
         if c.side:
             c.keep(*args, h0, lengths, y, hT, states, ws)
         st = lib.mi_selective_scan_fwd(*(_ptr(t) for t in args), _ptr(h0), _ptr(lengths), y.data_ptr(),
                                        hT.data_ptr(), _ptr(states), Bn, T, D, G, N, int(bool(softplus)), dt,
-                                       ws.data_ptr(), _nbytes(ws), c.handle)
+                                       _ptr(ws), 0 if ws is None else _nbytes(ws), c.handle)
         if st:
             _check(st, "mi_selective_scan_fwd")
     return y, hT, states

@@ -56,30 +56,53 @@ __device__ __forceinline__ int64_t seq_len(const int32_t *lengths, int64_t b, in
 // workgroup, four threads a column that each add every fourth row, joined in a
 // fixed order.  Reads each partial once with 256-byte rows.
 template <class Store>
-__global__ __launch_bounds__(256) void reduce_parts_kernel(const float *part, int64_t P, int64_t M, Store st) {
+struct ReduceJob {
+    const float *part;
+    int64_t P, M;
+    Store st;
+    int blocks;  // workgroups of this job
+};
+constexpr int64_t REDUCE_BLOCKS = 16384;
+
+template <class Store>
+__device__ __forceinline__ void reduce_job(const ReduceJob<Store> &j, int block) {
     __shared__ float acc[4][64];
     const int col = threadIdx.x & 63, row = threadIdx.x >> 6;
-    for (int64_t m0 = (int64_t)blockIdx.x * 64; m0 < M; m0 += (int64_t)gridDim.x * 64) {
+    for (int64_t m0 = (int64_t)block * 64; m0 < j.M; m0 += (int64_t)j.blocks * 64) {
         const int64_t m = m0 + col;
         float s = 0.f;
-        if (m < M) {
-            const float *q = part + m;
+        if (m < j.M) {
+            const float *q = j.part + m;
 #pragma unroll 4
-            for (int64_t p = row; p < P; p += 4) s += q[p * M];
+            for (int64_t p = row; p < j.P; p += 4) s += q[p * j.M];
         }
         acc[row][col] = s;
         __syncthreads();
-        if (row == 0 && m < M) st(m, (acc[0][col] + acc[1][col]) + (acc[2][col] + acc[3][col]));
+        if (row == 0 && m < j.M) j.st(m, (acc[0][col] + acc[1][col]) + (acc[2][col] + acc[3][col]));
         __syncthreads();
     }
 }
+template <class Store>
+__global__ __launch_bounds__(256) void reduce_parts_kernel(ReduceJob<Store> j) {
+    reduce_job(j, (int)blockIdx.x);
+}
+// Two sums in one launch.
+template <class S1, class S2>
+__global__ __launch_bounds__(256) void reduce_two_kernel(ReduceJob<S1> a, ReduceJob<S2> b) {
+    if ((int)blockIdx.x < a.blocks) reduce_job(a, (int)blockIdx.x);
+    else reduce_job(b, (int)blockIdx.x - a.blocks);
+}
 
 template <class Store>
-inline mi_status reduce_parts(const float *part, int64_t P, int64_t M, Store st, hipStream_t s) {
-    if (M == 0) return MI_OK;
+inline ReduceJob<Store> reduce_of(const float *part, int64_t P, int64_t M, Store st) {
     const int64_t blocks = (M + 63) / 64;
-    hipLaunchKernelGGL(reduce_parts_kernel<Store>, dim3((unsigned)(blocks < 16384 ? blocks : 16384)), dim3(256), 0,
-                       s, part, P, M, st);
+    return {part, P, M, st, (int)(blocks < REDUCE_BLOCKS ? blocks : REDUCE_BLOCKS)};
+}
+template <class Store>
+inline mi_status reduce_parts(const float *part, int64_t P, int64_t M, Store st, hipStream_t s) {
+    const ReduceJob<Store> j = reduce_of(part, P, M, st);
+    if (j.blocks == 0) return MI_OK;
+    hipLaunchKernelGGL(reduce_parts_kernel<Store>, dim3((unsigned)j.blocks), dim3(256), 0, s, j);
     return launch_status();
 }
 

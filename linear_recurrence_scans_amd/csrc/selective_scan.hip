@@ -438,7 +438,8 @@ FwdPlan fwd_plan(int64_t B, int64_t G, int64_t per, int64_t T) {
     if (narrow >= 192) return {FWD_NARROW, 1};
     const int64_t blocks = (T + 4 * L - 1) / (4 * L), want = (768 + n - 1) / n;
     const int64_t seg = (blocks + want - 1) / want;  // blocks a segment
-    return {FWD_SEGMENTS, blocks < 2 || seg < 1 ? 1 : (blocks + seg - 1) / seg};
+    // (a second launch costs the host about two blocks' time, its segments two more)
+    return {FWD_SEGMENTS, blocks < 8 ? 1 : (blocks + seg - 1) / seg};
 }
 int64_t fwd_segments(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N) {
     switch (scan_s(N)) {

@@ -684,7 +684,7 @@ int64_t bwd_tiles(int64_t per, int64_t N) {
 // LDS holds one a CU), else as many as make 256.
 int64_t bwd_segments(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N) {
     const int64_t n = B * G * bwd_tiles(D / G, N), blk = scan_block(N), blocks = (T + blk - 1) / blk;
-    if (n >= 192 || blocks < 2) return 1;
+    if (n >= 192 || blocks < 3) return 1;  // (a launch costs the host about half a block's time)
     const int64_t want = (256 + n - 1) / n, seg = (blocks + want - 1) / want;
     return (blocks + seg - 1) / seg;
 }
@@ -716,19 +716,23 @@ mi_status launch_bwd(ScanArgs a, hipStream_t s) {
     return launch_status();
 }
 template <typename T>
-mi_status launch_bwd_t(const ScanArgs &a, void *dBm, void *dCm, hipStream_t s) {
-    mi_status st;
-    switch (scan_s(a.N)) {
-        case 1: st = launch_bwd<T, 1>(a, s); break;
-        case 2: st = launch_bwd<T, 2>(a, s); break;
-        case 4: st = launch_bwd<T, 4>(a, s); break;
-        case 8: st = launch_bwd<T, 8>(a, s); break;
-        default: st = launch_bwd<T, 16>(a, s);
-    }
+mi_status launch_bwd_t(const ScanArgs &a, void *dBm, void *dCm, const StoreParams &params, hipStream_t s) {
+    mi_status st = MI_OK;
+    if (a.B > 0) switch (scan_s(a.N)) {
+            case 1: st = launch_bwd<T, 1>(a, s); break;
+            case 2: st = launch_bwd<T, 2>(a, s); break;
+            case 4: st = launch_bwd<T, 4>(a, s); break;
+            case 8: st = launch_bwd<T, 8>(a, s); break;
+            default: st = launch_bwd<T, 16>(a, s);
+        }
     if (st != MI_OK) return st;
     const int64_t bc = a.B * a.T * a.G * a.N;
-    return reduce_parts(a.part_bc, bwd_tiles(a.per, a.N), 2 * bc,
-                        StoreShared<T>{static_cast<T *>(dBm), static_cast<T *>(dCm), bc}, s);
+    const auto shared = reduce_of(a.part_bc, bwd_tiles(a.per, a.N), 2 * bc,
+                                  StoreShared<T>{static_cast<T *>(dBm), static_cast<T *>(dCm), bc});
+    const auto own = reduce_of(a.part_a, a.B * a.n_seg, (a.N + 2) * a.D, params);
+    hipLaunchKernelGGL((reduce_two_kernel<StoreShared<T>, StoreParams>), dim3((unsigned)(shared.blocks + own.blocks)),
+                       dim3(256), 0, s, shared, own);
+    return launch_status();
 }
 
 // Workspace: partial dBm and dCm; partial dA, dskip, ddelta_bias; the segments'
@@ -800,12 +804,11 @@ mi_status mi_selective_scan_bwd(const void *u, const void *delta, const float *A
         a.n_seg = (int)w.n_seg;
         a.seg_v = reinterpret_cast<float *>(static_cast<char *>(ws) + w.bc + w.a);
         a.seg_p = a.seg_v + w.n_seg * B * D * N;
-        if (dt == MI_F32) st = launch_bwd_t<float>(a, dBm, dCm, stream);
-        else if (dt == MI_BF16) st = launch_bwd_t<bf16_t>(a, dBm, dCm, stream);
-        else st = launch_bwd_t<f16_t>(a, dBm, dCm, stream);
-        if (st != MI_OK) return st;
     }
-    return reduce_parts(a.part_a, B * (B > 0 ? a.n_seg : 1), (N + 2) * D, StoreParams{dA, dskip, ddelta_bias, D, N}, stream);
+    const StoreParams params{dA, dskip, ddelta_bias, D, N};
+    if (dt == MI_F32) return launch_bwd_t<float>(a, dBm, dCm, params, stream);
+    if (dt == MI_BF16) return launch_bwd_t<bf16_t>(a, dBm, dCm, params, stream);
+    return launch_bwd_t<f16_t>(a, dBm, dCm, params, stream);
 }
 
 }  // extern "C"
