@@ -11,7 +11,6 @@
 #include <algorithm>
 #include <mutex>
 
-#include "checks.hpp"
 #include "common.hpp"
 #include "internal.hpp"
 
@@ -44,6 +43,65 @@ mi_status zero_async(void *p, size_t bytes, hipStream_t s) {
 }
 
 namespace {
+
+size_t elem_size(mi_dtype dt) { return dt == MI_F32 ? 4 : 2; }
+bool dtype_known(mi_dtype dt) { return dt == MI_F32 || dt == MI_BF16 || dt == MI_F16; }
+
+// a*b*c*d into *out without int64 overflow; all factors non-negative.
+bool mul_ok(int64_t a, int64_t b, int64_t c, int64_t d, int64_t *out) {
+    int64_t r;
+    if (__builtin_mul_overflow(a, b, &r)) return false;
+    if (__builtin_mul_overflow(r, c, &r)) return false;
+    if (__builtin_mul_overflow(r, d, &r)) return false;
+    *out = r;
+    return true;
+}
+
+struct Buf {
+    const void *p;
+    int64_t bytes;
+};
+
+bool overlaps(const Buf &x, const Buf &y) {
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(x.p), b0 = reinterpret_cast<uintptr_t>(y.p);
+    return a0 < b0 + (uintptr_t)y.bytes && b0 < a0 + (uintptr_t)x.bytes;
+}
+
+// Null, misaligned or overlapping buffers.  `n_out` trailing entries of `bufs`
+// are outputs: an output may overlap nothing else.
+mi_status check_buffers(const Buf *bufs, int n, int n_out, size_t align) {
+    for (int i = 0; i < n; ++i) {
+        if (bufs[i].p == nullptr) return MI_ERR_INVALID_ARG;
+        if (reinterpret_cast<uintptr_t>(bufs[i].p) % align != 0) return MI_ERR_INVALID_ARG;
+    }
+    for (int i = n - n_out; i < n; ++i)
+        for (int j = 0; j < n; ++j)
+            if (j != i && overlaps(bufs[i], bufs[j])) return MI_ERR_INVALID_ARG;
+    return MI_OK;
+}
+
+mi_status check_ws(void *ws, size_t ws_bytes, size_t need, const Buf *bufs, int n) {
+    if (ws == nullptr || ws_bytes < need) return MI_ERR_WORKSPACE;
+    if (reinterpret_cast<uintptr_t>(ws) % 256 != 0) return MI_ERR_INVALID_ARG;
+    Buf w{ws, (int64_t)ws_bytes};
+    for (int i = 0; i < n; ++i)
+        if (overlaps(w, bufs[i])) return MI_ERR_INVALID_ARG;
+    return MI_OK;
+}
+
+// Widest vector (elements per lane) such that D is a multiple of it and every
+// pointer is aligned to the access width; 16-byte accesses at most.
+int pick_vec(int64_t D, size_t esize, const Buf *bufs, int n) {
+    const int maxv = (int)(16 / esize);
+    for (int v = maxv; v > 1; v /= 2) {
+        if (D % v != 0) continue;
+        bool ok = true;
+        for (int i = 0; i < n && ok; ++i)
+            ok = reinterpret_cast<uintptr_t>(bufs[i].p) % (v * esize) == 0;
+        if (ok) return v;
+    }
+    return 1;
+}
 
 // Shared validation of the (B, T, D) channel ops.  Returns MI_OK and sets
 // *empty when there is nothing to do.

@@ -1,5 +1,6 @@
-// checks.hpp -- host-side argument checks shared by the entry points: sizes,
-// pointers, overlaps, workspaces and the vector width a layout allows.
+// checks.hpp -- host-side argument checks of the block operators' entry points:
+// sizes, pointers, overlaps, workspaces and the vector width a layout allows.
+// (The scans' entry points have theirs in api.hip.)
 #pragma once
 
 #include <stddef.h>
@@ -30,19 +31,6 @@ struct Buf {
 inline bool overlaps(const Buf &x, const Buf &y) {
     const uintptr_t a0 = reinterpret_cast<uintptr_t>(x.p), b0 = reinterpret_cast<uintptr_t>(y.p);
     return a0 < b0 + (uintptr_t)y.bytes && b0 < a0 + (uintptr_t)x.bytes;
-}
-
-// Null, misaligned or overlapping buffers.  `n_out` trailing entries of `bufs`
-// are outputs: an output may overlap nothing else.
-inline mi_status check_buffers(const Buf *bufs, int n, int n_out, size_t align) {
-    for (int i = 0; i < n; ++i) {
-        if (bufs[i].p == nullptr) return MI_ERR_INVALID_ARG;
-        if (reinterpret_cast<uintptr_t>(bufs[i].p) % align != 0) return MI_ERR_INVALID_ARG;
-    }
-    for (int i = n - n_out; i < n; ++i)
-        for (int j = 0; j < n; ++j)
-            if (j != i && overlaps(bufs[i], bufs[j])) return MI_ERR_INVALID_ARG;
-    return MI_OK;
 }
 
 inline mi_status check_ws(void *ws, size_t ws_bytes, size_t need, const Buf *bufs, int n) {
