@@ -51,7 +51,8 @@ typedef enum {
     MI_ERR_INVALID_ARG = 1, /* null pointer, negative size, byte-size overflow,
                                misaligned element pointer, overlapping buffers */
     MI_ERR_UNSUPPORTED = 2, /* outside the envelope: k not in [1,16], v not in
-                               [1,128], or a dtype not built for the op */
+                               [1,128], a limit that a block operator states
+                               below, or a dtype not built for the op */
     MI_ERR_WORKSPACE = 3,   /* workspace NULL or smaller than the query says */
     MI_ERR_LAUNCH = 4,      /* the HIP runtime reported an error at launch */
     MI_ERR_DEVICE = 5,      /* no usable gfx950 device */
@@ -279,7 +280,8 @@ mi_status mi_causal_conv_step(const void *x, const float *w, const float *bias, 
 /* Selective state-space scan: N states a channel, with gates formed from the
  * token.  u, delta, z (B,T,D); A (D,N); Bm, Cm (B,T,G,N), one row for the D/G
  * channels of a group; skip, delta_bias (D); h0, hT (B,D,N).  z, skip,
- * delta_bias, h0, hT may be NULL.  1 <= N <= 64, G divides D.
+ * delta_bias, h0, hT may be NULL.  1 <= N <= 64, G divides D, and D and G N
+ * are at most 2^24.
  *     dl_t = softplus(delta_t + delta_bias)       (softplus = 0: delta + bias)
  *     h_t[n] = exp(dl_t A[n]) h_{t-1}[n] + dl_t u_t Bm_t[n],   h_0 = h0
  *     s_t = sum_n Cm_t[n] h_t[n] + skip u_t,   y_t = s_t silu(z_t)

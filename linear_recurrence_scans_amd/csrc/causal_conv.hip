@@ -5,7 +5,11 @@
 // VEC consecutive channels (16 bytes), a wave R consecutive steps, and the K - 1
 // steps before them are read again (they are in the caches: the neighbouring
 // wave reads them too).  All of a wave's rows are loaded before the first is
-// used, so a wave keeps R + K - 1 rows in flight.
+// used, so a wave keeps R + K - 1 rows in flight.  Measured (MI355X, K = 4, SiLU,
+// bf16): B = 8, T = 8192, D = 4096 207 us, 5.2 TB/s of x and y, a little above a
+// large copy's 4.9; 8, 12 and 32 steps a wave take 263, 231 and 210 us.  The
+// gradient at B = 4, T = 4096, D = 2048 takes 50 us (4.0 TB/s of x, dy and dx; the
+// vector ALU is busy for two thirds of it) and its sums 5.
 #include "block_ops.hpp"
 #include "checks.hpp"
 

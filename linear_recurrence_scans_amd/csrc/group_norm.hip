@@ -6,7 +6,8 @@
 // sums (the variance about the mean, no cancellation).  A lane keeps its
 // channels' parameters, and in the backward their gradients' sums, in registers
 // over all the rows its workgroup walks.  The bound is HBM: forward 2 to 3,
-// backward 3 to 5 tensors moved once.
+// backward 3 to 5 tensors moved once.  Measured (MI355X, 16384 x 4096 bf16, 32
+// groups, gated): forward 75 us (5.4 TB/s), backward 138 (4.9 TB/s) and its sums 7.
 #include "block_ops.hpp"
 #include "checks.hpp"
 
