@@ -2,14 +2,15 @@
 // with an optional SiLU; its gradient; and its single-token step.
 //
 // The forward streams x once and writes y once: the bound is HBM.  A lane owns
-// VEC consecutive channels (16 bytes), a wave R consecutive steps, and the K - 1
+// VEC consecutive channels (8 bytes), a wave R consecutive steps, and the K - 1
 // steps before them are read again (they are in the caches: the neighbouring
 // wave reads them too).  All of a wave's rows are loaded before the first is
 // used, so a wave keeps R + K - 1 rows in flight.  Measured (MI355X, K = 4, SiLU,
-// bf16): B = 8, T = 8192, D = 4096 207 us, 5.2 TB/s of x and y, a little above a
-// large copy's 4.9; 8, 12 and 32 steps a wave take 263, 231 and 210 us.  The
-// gradient at B = 4, T = 4096, D = 2048 takes 50 us (4.0 TB/s of x, dy and dx; the
-// vector ALU is busy for two thirds of it) and its sums 5.
+// bf16): B = 8, T = 8192, D = 4096 204 us, 5.3 TB/s of x and y, a little above a
+// large copy's 4.9; with 16 bytes a lane (140 registers for 74) 211 us, with 8, 24
+// and 32 steps a wave 218, 206 and 214 us.  Forward and backward at B = 4, T = 4096,
+// D = 2048 together 72 to 79 us; with 16 bytes and 8 steps a batch in the backward
+// (115 registers for 98) 87 us.
 #include "block_ops.hpp"
 #include "checks.hpp"
 
@@ -127,7 +128,7 @@ template <typename T, int VEC, int K>
 __global__ __launch_bounds__(CONV_NW * 64) void conv_bwd_kernel(ConvArgs p) {
     using PK = Pack<T, VEC>;
     using raw_t = typename PK::raw_t;
-    constexpr int U = K * ((8 + K - 1) / K);  // steps an iteration: whole turns of the windows
+    constexpr int U = K * ((4 + K - 1) / K);  // steps an iteration: whole turns of the windows
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int item = blockIdx.x;
@@ -358,19 +359,19 @@ mi_status mi_causal_conv_fwd(const void *x, const float *w, const float *bias, c
     if (K > 1) out.opt(xT, s.state, es);
     if ((st = check_lists(in, out)) != MI_OK) return st;
     const Buf act_bufs[4] = {{x, s.x}, {K > 1 ? x0 : nullptr, s.state}, {y, s.x}, {K > 1 ? xT : nullptr, s.state}};
-    const int maxv = (int)(16 / es);
-    const bool wide = pick_vec(D, es, act_bufs, 4) == maxv;
+    const int half = (int)(8 / es);
+    const bool wide = pick_vec(D, es, act_bufs, 4) >= half;
     ConvArgs a{};
     a.x = x; a.w = w; a.bias = bias; a.x0 = x0; a.lengths = lengths; a.y = y; a.xT = xT;
     a.T = T; a.D = D; a.act = act;
-    const int64_t tile = 64 * (wide ? maxv : 1);
+    const int64_t tile = 64 * (wide ? half : 1);
     const int64_t n_dt = (D + tile - 1) / tile, n_tt = time_tiles(T, CONV_NW * CONV_FWD_R);
     int64_t grid;
     if (!mul_ok(B, n_dt, n_tt, 1, &grid) || grid > MAX_GRID) return MI_ERR_UNSUPPORTED;
     a.n_dt = (int)n_dt; a.n_tt = (int)n_tt;
     return with_type(dt, K, [&](auto tag, auto num) {
         using T_ = typename decltype(tag)::type;
-        constexpr int K_ = decltype(num)::value, V = (int)(16 / sizeof(T_));
+        constexpr int K_ = decltype(num)::value, V = (int)(8 / sizeof(T_));
         if (wide)
             hipLaunchKernelGGL((conv_fwd_kernel<T_, V, K_>), dim3((unsigned)grid), dim3(CONV_NW * 64), 0, stream, a);
         else
