@@ -45,9 +45,10 @@ class _Here:
         return False
 
 
-# (tensors on a GPU have initialised torch's runtime, so the raw lookups are safe)
-_current_device = torch._C._cuda_getDevice
-_current_raw_stream = torch._C._cuda_getCurrentRawStream
+# (tensors on a GPU have initialised torch's runtime, so the raw lookups are safe;
+# a torch without GPU support has none, and no such tensors)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _call(stream, device):
