@@ -314,6 +314,14 @@ int bwd_rows(int64_t B, int64_t T, int64_t D, int64_t esize) {
     return r;
 }
 
+// Vector width: 8 bytes (wider ones cost the windows' registers), two elements or
+// one.  Forward and backward at B = 4, T = 4096, bf16: D = 4094 178 us in pairs and
+// 385 in single elements; D = 4092 146 in 8 bytes; D = 4095 389.
+int conv_vec(int64_t D, size_t es, const Buf *b, int n) {
+    const int v = pick_vec(D, es, b, n), half = (int)(8 / es);
+    return v >= half ? half : v >= 2 ? 2 : 1;
+}
+
 int64_t time_tiles(int64_t T, int64_t rows) {
     const int64_t n = (T + rows - 1) / rows;
     return n < 1 ? 1 : n;  // an empty sequence still writes its state
@@ -359,12 +367,11 @@ mi_status mi_causal_conv_fwd(const void *x, const float *w, const float *bias, c
     if (K > 1) out.opt(xT, s.state, es);
     if ((st = check_lists(in, out)) != MI_OK) return st;
     const Buf act_bufs[4] = {{x, s.x}, {K > 1 ? x0 : nullptr, s.state}, {y, s.x}, {K > 1 ? xT : nullptr, s.state}};
-    const int half = (int)(8 / es);
-    const bool wide = pick_vec(D, es, act_bufs, 4) >= half;
+    const int vec = conv_vec(D, es, act_bufs, 4);
     ConvArgs a{};
     a.x = x; a.w = w; a.bias = bias; a.x0 = x0; a.lengths = lengths; a.y = y; a.xT = xT;
     a.T = T; a.D = D; a.act = act;
-    const int64_t tile = 64 * (wide ? half : 1);
+    const int64_t tile = 64 * vec;
     const int64_t n_dt = (D + tile - 1) / tile, n_tt = time_tiles(T, CONV_NW * CONV_FWD_R);
     int64_t grid;
     if (!mul_ok(B, n_dt, n_tt, 1, &grid) || grid > MAX_GRID) return MI_ERR_UNSUPPORTED;
@@ -372,8 +379,10 @@ mi_status mi_causal_conv_fwd(const void *x, const float *w, const float *bias, c
     return with_type(dt, K, [&](auto tag, auto num) {
         using T_ = typename decltype(tag)::type;
         constexpr int K_ = decltype(num)::value, V = (int)(8 / sizeof(T_));
-        if (wide)
+        if (vec == V)
             hipLaunchKernelGGL((conv_fwd_kernel<T_, V, K_>), dim3((unsigned)grid), dim3(CONV_NW * 64), 0, stream, a);
+        else if (vec == 2)
+            hipLaunchKernelGGL((conv_fwd_kernel<T_, 2, K_>), dim3((unsigned)grid), dim3(CONV_NW * 64), 0, stream, a);
         else
             hipLaunchKernelGGL((conv_fwd_kernel<T_, 1, K_>), dim3((unsigned)grid), dim3(CONV_NW * 64), 0, stream, a);
         return launch_status();
@@ -424,9 +433,8 @@ mi_status mi_causal_conv_bwd(const void *x, const float *w, const float *bias, c
         const bool state = K > 1;
         const Buf act_bufs[6] = {{x, s.x},   {dy, s.x}, {dx, s.x}, {state ? x0 : nullptr, s.state},
                                  {state ? dxT : nullptr, s.state}, {state ? dx0 : nullptr, s.state}};
-        const int half = (int)(8 / es);  // 8-byte vectors: four windows of K rows have to fit the registers
-        const bool wide = pick_vec(D, es, act_bufs, 6) >= half;
-        const int64_t tile = 64 * (wide ? half : 1);
+        const int vec = conv_vec(D, es, act_bufs, 6);
+        const int64_t tile = 64 * vec;
         const int64_t n_dt = (D + tile - 1) / tile;
         int64_t grid;
         if (!mul_ok(B, n_dt, n_tt, 1, &grid) || grid > MAX_GRID) return MI_ERR_UNSUPPORTED;
@@ -434,8 +442,10 @@ mi_status mi_causal_conv_bwd(const void *x, const float *w, const float *bias, c
         st = with_type(dt, K, [&](auto tag, auto num) {
             using T_ = typename decltype(tag)::type;
             constexpr int K_ = decltype(num)::value, V = (int)(8 / sizeof(T_));
-            if (wide)
+            if (vec == V)
                 hipLaunchKernelGGL((conv_bwd_kernel<T_, V, K_>), dim3((unsigned)grid), dim3(CONV_NW * 64), 0, stream, a);
+            else if (vec == 2)
+                hipLaunchKernelGGL((conv_bwd_kernel<T_, 2, K_>), dim3((unsigned)grid), dim3(CONV_NW * 64), 0, stream, a);
             else
                 hipLaunchKernelGGL((conv_bwd_kernel<T_, 1, K_>), dim3((unsigned)grid), dim3(CONV_NW * 64), 0, stream, a);
             return launch_status();
@@ -460,18 +470,19 @@ mi_status mi_causal_conv_step(const void *x, const float *w, const float *bias, 
     }
     if ((st = check_lists(in, out)) != MI_OK) return st;
     const Buf act_bufs[4] = {{x, s.x}, {y, s.x}, {K > 1 ? x0 : nullptr, s.state}, {K > 1 ? x_out : nullptr, s.state}};
-    const int half = (int)(8 / es);
-    const bool wide = pick_vec(D, es, act_bufs, 4) >= half;
+    const int vec = conv_vec(D, es, act_bufs, 4);
     ConvArgs a{};
     a.x = x; a.w = w; a.bias = bias; a.x0 = x0; a.y = y; a.xT = x_out; a.T = 1; a.D = D; a.act = act;
-    const int64_t n = B * D / (wide ? half : 1);
+    const int64_t n = B * D / vec;
     const int64_t grid = (n + 255) / 256;
     if (grid > MAX_GRID) return MI_ERR_UNSUPPORTED;
     return with_type(dt, K, [&](auto tag, auto num) {
         using T_ = typename decltype(tag)::type;
         constexpr int K_ = decltype(num)::value, V = (int)(8 / sizeof(T_));
-        if (wide)
+        if (vec == V)
             hipLaunchKernelGGL((conv_step_kernel<T_, V, K_>), dim3((unsigned)grid), dim3(256), 0, stream, a, n);
+        else if (vec == 2)
+            hipLaunchKernelGGL((conv_step_kernel<T_, 2, K_>), dim3((unsigned)grid), dim3(256), 0, stream, a, n);
         else
             hipLaunchKernelGGL((conv_step_kernel<T_, 1, K_>), dim3((unsigned)grid), dim3(256), 0, stream, a, n);
         return launch_status();

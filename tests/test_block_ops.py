@@ -362,6 +362,22 @@ def test_conv_channels(D):
 
 
 @gpu
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("D", [2, 6, 70, 126, 130, 258])
+def test_conv_pairs(D, dtype):
+    """Even widths that hold no whole 8-byte vectors in 16-bit types, and their steps."""
+    check_conv(2, 70, D, 4, dtype, "silu", D, lengths=[70, 33])
+    d = conv_inputs(3, 5, D, 4, dtype, D)
+    x, w, b = dev(d["x"], dtype), dev(d["w"], F32), dev(d["bias"], F32)
+    y, xT = lrs.mi_causal_conv_fwd(x, w, b, act="silu")
+    st = torch.zeros(3, 3, D, dtype=dtype, device="cuda")
+    for t in range(5):
+        yt, st = lrs.mi_causal_conv_step(x[:, t], w, b, st, act="silu")
+        assert torch.equal(yt, y[:, t])
+    assert torch.equal(st, xT)
+
+
+@gpu
 def test_conv_continues_and_steps():
     """Pieces and single steps give the whole's results, and the same carried inputs."""
     say("conv pieces and steps B=3 T=29 D=72 K=4 bf16")
