@@ -344,8 +344,11 @@ struct StoreNorm {
     }
 };
 
-// How a shape is cut: lanes a group (4, 16, 64, 256) and vectors a lane, the
-// smallest that hold a group; 0 vectors: the wide kernel.
+// How a shape is cut: lanes a group (1, 4, 16, 64, 256) and vectors a lane (up to
+// 8, or 16 of one or two elements), the smallest that hold a group; 0 vectors: the
+// wide kernel.  16384 rows bf16 with a gate, forward and backward: 4096 channels in
+// 512 groups, one vector each, 233 us with one lane a group and 466 with four; a
+// group of 4095 channels 1103 us with 16 elements a lane and 1690 in the wide kernel.
 struct NormPlan {
     int team, nv;
     int64_t slices, parts, rows;
@@ -353,9 +356,9 @@ struct NormPlan {
 NormPlan norm_plan(int64_t R, int64_t D, int64_t G, int vec, bool bwd) {
     NormPlan q;
     const int64_t dg = D / G, n = (dg + vec - 1) / vec;
-    q.team = n <= 4 ? 4 : n <= 16 ? 16 : n <= 64 ? 64 : 256;
+    q.team = n <= 1 ? 1 : n <= 4 ? 4 : n <= 16 ? 16 : n <= 64 ? 64 : 256;
     q.nv = 1;
-    while (q.nv < 8 && (int64_t)q.team * q.nv < n) q.nv *= 2;
+    while (q.nv < (vec <= 2 ? 16 : 8) && (int64_t)q.team * q.nv < n) q.nv *= 2;
     if ((int64_t)q.team * q.nv < n) q.nv = 0;
     int gps = 1;
     if (q.team < 64)
@@ -381,10 +384,11 @@ int norm_gps(const NormPlan &q, int64_t G) {
     return gps;
 }
 
-// Vector width: whole vectors a group, 16-byte aligned pointers; else single elements.
+// Vector width: 16 bytes, two elements or one, in whole vectors a group and as the
+// pointers are aligned.
 int norm_vec(int64_t D, int64_t G, size_t es, const Buf *b, int n) {
-    const int maxv = (int)(16 / es);
-    return (D / G) % maxv == 0 && pick_vec(D, es, b, n) == maxv ? maxv : 1;
+    const int maxv = (int)(16 / es), v = pick_vec(D, es, b, n);
+    return (D / G) % maxv == 0 && v == maxv ? maxv : (D / G) % 2 == 0 && v >= 2 ? 2 : 1;
 }
 
 template <typename T, int VEC, int NV, int TEAM, bool BWD>
@@ -399,6 +403,7 @@ mi_status launch_norm(const NormArgs &a, const NormPlan &q, unsigned grid, hipSt
         hipLaunchKernelGGL((norm_wide_kernel<T, BWD>), dim3(grid), dim3(256), 0, s, a);
         return launch_status();
     }
+    if (q.team == 1) return go<T, VEC, 1, 1, BWD>(a, grid, s);
     if (q.team == 4) return go<T, VEC, 1, 4, BWD>(a, grid, s);
     if (q.team == 16) return go<T, VEC, 1, 16, BWD>(a, grid, s);
     if (q.team == 64) return go<T, VEC, 1, 64, BWD>(a, grid, s);
@@ -407,6 +412,8 @@ mi_status launch_norm(const NormArgs &a, const NormPlan &q, unsigned grid, hipSt
         case 2: return go<T, VEC, 2, 256, BWD>(a, grid, s);
         case 4: return go<T, VEC, 4, 256, BWD>(a, grid, s);
     }
+    if constexpr (VEC <= 2)
+        if (q.nv == 16) return go<T, VEC, 16, 256, BWD>(a, grid, s);
     return go<T, VEC, 8, 256, BWD>(a, grid, s);
 }
 template <typename T, bool BWD>
@@ -420,7 +427,9 @@ mi_status run_norm(NormArgs a, int vec, hipStream_t s, int64_t *parts) {
     *parts = q.parts;
     if (grid == 0) return MI_OK;
     constexpr int V = (int)(16 / sizeof(T));
-    return vec == V ? launch_norm<T, V, BWD>(a, q, (unsigned)grid, s) : launch_norm<T, 1, BWD>(a, q, (unsigned)grid, s);
+    if (vec == V) return launch_norm<T, V, BWD>(a, q, (unsigned)grid, s);
+    if (vec == 2) return launch_norm<T, 2, BWD>(a, q, (unsigned)grid, s);
+    return launch_norm<T, 1, BWD>(a, q, (unsigned)grid, s);
 }
 template <bool BWD>
 mi_status run_norm(const NormArgs &a, mi_dtype dt, int vec, hipStream_t s, int64_t *parts) {
@@ -468,7 +477,7 @@ size_t mi_group_norm_bwd_workspace(int64_t R, int64_t D, int64_t G, mi_dtype dt)
     int64_t bytes;
     if (check_norm(R, D, G, 0.f, MI_ACT_NONE, nullptr, dt, &bytes) != MI_OK || R == 0 || D == 0) return 0;
     int64_t need = 0;
-    for (int vec : {1, (int)(16 / elem_size(dt))}) {  // pointers decide the width: the larger of both
+    for (int vec : {1, 2, (int)(16 / elem_size(dt))}) {  // pointers decide the width: the largest need
         const NormPlan q = norm_plan(R, D, G, vec, true);
         int64_t n;
         if (!mul_ok(q.parts, D, 8, 1, &n)) return 0;

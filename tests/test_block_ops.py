@@ -583,6 +583,16 @@ def test_norm_groups(D, G, dtype):
 
 
 @gpu
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("D,G", [(2, 1), (10, 5), (24, 4), (512, 64), (600, 75), (3, 3), (130, 65), (2047, 1), (2050, 1),
+                                 (4095, 1), (4094, 2), (4098, 1), (8190, 1), (8194, 1), (16390, 1)])
+def test_norm_odd_widths(D, G, dtype):
+    """Groups of single elements, pairs and whole vectors, one vector a group, both sides of each limit."""
+    check_norm(4, D, G, dtype, D + G, z=True)
+    check_norm(71, D, G, dtype, D + G + 1, centered=False, act="silu")
+
+
+@gpu
 @pytest.mark.parametrize("rows", [0, 1, 2, 3, 7, 16, 33, 130])
 def test_norm_rows(rows):
     check_norm(rows, 48, 3, F32, rows, act="silu")
