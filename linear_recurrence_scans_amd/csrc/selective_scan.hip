@@ -81,7 +81,7 @@ __global__ __launch_bounds__(NW * 64, WPS) void scan_fwd_kernel(ScanArgs p) {
             const float *v = p.seg_v + st_base + st_off[f], *q = p.seg_p + st_base + st_off[f];
 #pragma unroll 4
             for (int k = 0; k < seg; ++k)
-                carry[f] = fmaf(q[k * p.B * p.D * p.N], carry[f], v[k * p.B * p.D * p.N]);
+                carry[f] = carry_through(q[k * p.B * p.D * p.N], carry[f], v[k * p.B * p.D * p.N]);
         }
         prod[f] = 1.f;
     }
@@ -208,7 +208,7 @@ __global__ __launch_bounds__(NW * 64, WPS) void scan_fwd_kernel(ScanArgs p) {
 #pragma unroll
             for (int s = 0; s < S; ++s) {
                 hv[c * S + s] = h[s][c];
-                pv[c * S + s] = __builtin_amdgcn_exp2f(sum[c] * A2[s][c]);
+                pv[c * S + s] = SUM ? root_product(sum[c] * A2[s][c]) : __builtin_amdgcn_exp2f(sum[c] * A2[s][c]);
             }
         LV::write(sm_s[wave], lane, hv);
         LV::write(sm_p[wave], lane, pv);
@@ -223,21 +223,45 @@ __global__ __launch_bounds__(NW * 64, WPS) void scan_fwd_kernel(ScanArgs p) {
                     sv[w] = sm_s[w][i];
                     pw[w] = sm_p[w][i];
                 }
+                if constexpr (SUM) {
 #pragma unroll
-                for (int w = 0; w < NW; ++w) {
-                    if (SUM) {
-                        prod[f] *= pw[w];
+                    for (int w = 0; w < NW; ++w) {
+                        prod[f] = join_roots(prod[f], pw[w]);
+                        c = carry_through(pw[w], c, sv[w]);
+                    }
+                } else {
+                    // state v enters wave w
+                    const auto enter = [&](int w, float v) {
+                        if ((w * L) % scan_block_of<S>() % (NW * L) == 0 && (tb + w * L) % scan_block_of<S>() == 0 &&
+                            p.states && st_off[f] >= 0 && tb + w * L < p.T) {
+                            const int64_t blk = (tb + w * L) / scan_block_of<S>();
+                            const int64_t n_blk = (p.T + scan_block_of<S>() - 1) / scan_block_of<S>();
+                            p.states[(b * n_blk + blk) * p.D * p.N + d0 * p.N + st_off[f]] = v;
+                        }
+                        sm_s[w][i] = v;
+                    };
+#pragma unroll
+                    for (int w = 0; w < NW; ++w) {
+                        enter(w, c);
                         c = fmaf(pw[w], c, sv[w]);
-                        continue;
                     }
-                    if ((w * L) % scan_block_of<S>() % (NW * L) == 0 && (tb + w * L) % scan_block_of<S>() == 0 &&
-                        p.states && st_off[f] >= 0 && tb + w * L < p.T) {
-                        const int64_t blk = (tb + w * L) / scan_block_of<S>();
-                        const int64_t n_blk = (p.T + scan_block_of<S>() - 1) / scan_block_of<S>();
-                        p.states[(b * n_blk + blk) * p.D * p.N + d0 * p.N + st_off[f]] = c;
+                    // a product out of range: step by step
+                    if (__builtin_expect(!__builtin_isfinite(c), 0)) {
+                        int ln, e;
+                        LV::where(i, &ln, &e);
+                        const int n = (ln >> 4) * S + e % S, q = e / S;
+                        const float a2 = st_off[f] >= 0 ? p.A[d0 * p.N + st_off[f]] * LOG2E : 0.f;
+                        c = carry[f];
+#pragma unroll 1
+                        for (int w = 0; w < NW; ++w) {
+                            enter(w, c);
+#pragma unroll 1
+                            for (int t = 0; t < L; ++t) {
+                                const float *x = sm_x[w][t][ln & 15];
+                                c = fmaf(__builtin_amdgcn_exp2f(x[q] * a2), c, sm_b[w][n][t] * x[C + q]);
+                            }
+                        }
                     }
-                    sm_s[w][i] = c;
-                    c = fmaf(pw[w], c, sv[w]);
                 }
                 carry[f] = c;
             }

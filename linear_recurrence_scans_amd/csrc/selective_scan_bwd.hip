@@ -204,7 +204,7 @@ __global__ __launch_bounds__(NW * 64) void scan_bwd_sum_kernel(ScanArgs p) {
 #pragma unroll
         for (int c = 0; c < C; ++c)
 #pragma unroll
-            for (int s = 0; s < S; ++s) pv[c * S + s] = __builtin_amdgcn_exp2f(sum[c] * A2[s][c]);
+            for (int s = 0; s < S; ++s) pv[c * S + s] = root_product(sum[c] * A2[s][c]);
         LV::write(sm_r[wave], lane, gv);
         LV::write(sm_p[wave], lane, pv);
         wg_lds_sync();
@@ -214,8 +214,8 @@ __global__ __launch_bounds__(NW * 64) void scan_bwd_sum_kernel(ScanArgs p) {
             if (i < E) {
 #pragma unroll
                 for (int w = NW - 1; w >= 0; --w) {
-                    edge[f] = fmaf(sm_p[w][i], edge[f], sm_r[w][i]);
-                    prod[f] *= sm_p[w][i];
+                    edge[f] = carry_through(sm_p[w][i], edge[f], sm_r[w][i]);
+                    prod[f] = join_roots(prod[f], sm_p[w][i]);
                 }
             }
         }
@@ -299,7 +299,7 @@ __global__ __launch_bounds__(NW * 64, 2) void scan_bwd_kernel(ScanArgs p) {
             const float *v = p.seg_v + st_base + st_off[f], *q = p.seg_p + st_base + st_off[f];
 #pragma unroll 4
             for (int k = p.n_seg - 1; k > seg; --k)
-                edge[f] = fmaf(q[k * p.B * p.D * p.N], edge[f], v[k * p.B * p.D * p.N]);
+                edge[f] = carry_through(q[k * p.B * p.D * p.N], edge[f], v[k * p.B * p.D * p.N]);
         }
     }
     const uint32_t row = (uint32_t)(p.D * (int64_t)sizeof(T));
@@ -453,7 +453,7 @@ __global__ __launch_bounds__(NW * 64, 2) void scan_bwd_kernel(ScanArgs p) {
 #pragma unroll
             for (int c = 0; c < C; ++c)
 #pragma unroll
-                for (int s = 0; s < S; ++s) hv[c * S + s] = __builtin_amdgcn_exp2f(sum[c] * A2[s][c]);
+                for (int s = 0; s < S; ++s) hv[c * S + s] = root_product(sum[c] * A2[s][c]);
             LV::write(my.p, lane, hv);
         }
         wg_lds_sync();
@@ -476,16 +476,16 @@ __global__ __launch_bounds__(NW * 64, 2) void scan_bwd_kernel(ScanArgs p) {
 #pragma unroll
                     for (int w = NW - 1; w >= 0; --w) {
                         val[w] = c;
-                        c = fmaf(pw[w], c, v[w]);
+                        c = carry_through(pw[w], c, v[w]);
                     }
-                    edge[f] = c;
                 } else {
 #pragma unroll
                     for (int w = 0; w < NW; ++w) {
                         val[w] = c;
-                        c = fmaf(pw[w], c, v[w]);
+                        c = carry_through(pw[w], c, v[w]);
                     }
                 }
+                if (rev) edge[f] = c;
             }
         }
         wg_lds_sync();

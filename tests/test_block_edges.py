@@ -1,0 +1,113 @@
+"""Block operators where they can go wrong: gates that grow, rates that vanish,
+limits of a launch, and the ways a call is cut that small shapes do not reach.
+
+References and bounds are those of tests/block_ref.py."""
+import pytest
+import torch
+
+import block_ref as R
+import linear_recurrence_scans_amd as lrs
+from test_block_ops import BF16, F16, F32, NAMES, dev, quant, say, scan_inputs
+
+gpu = pytest.mark.gpu
+
+
+def run_scan(d, dtype, softplus=True, lengths=None, backward=True):
+    """Forward (and backward) of the library on the float64 inputs d: (outputs, gradients)."""
+    par = ("A", "skip", "delta_bias", "h0", "dhT")
+    t = {k: dev(v, F32 if k in par else dtype) for k, v in d.items() if k != "lengths"}
+    ln = None if lengths is None else torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    args, rest = [t[k] for k in NAMES[:5]], {k: t[k] for k in NAMES[5:]}
+    out = lrs.mi_selective_scan_fwd(*args, **rest, softplus=softplus, lengths=ln, save_states=True)
+    if not backward:
+        return out, None
+    return out, lrs.mi_selective_scan_bwd(*args, out[2], t["dy"], t["dhT"], **rest, softplus=softplus, lengths=ln)
+
+
+# ---------------------------------------------------------------------------
+# gates above one
+# ---------------------------------------------------------------------------
+
+# One shape for each number of states a lane holds, in every way that the forward
+# is cut: segments of the sequence, narrow tiles, wide tiles.
+CUTS = [(B, T, D, N) for N in (1, 6, 16, 20, 40)
+        for B, T, D in ((1, 600, 16), (4, 70, 800), (16, 40, 1280))]
+
+
+def _growing(B, T, D, N, dtype):
+    """Every gate is e^30, and only the last two inputs and the first two upstream
+    gradients are not zero: states and gradients stay below e^60 although the
+    product of any three gates is past fp32's range."""
+    d = scan_inputs(B, T, D, 1, N, dtype, B + T + N, skip=False, z=False, bias=False, h0=True)
+    d["delta"], d["A"] = torch.full_like(d["delta"], 0.5), quant(60.0 + 0.1 * torch.rand(D, N, dtype=torch.float64,
+                                                                 generator=torch.Generator().manual_seed(N)), F32)
+    d["u"][:, :-2] = 0
+    d["dy"][:, 2:] = 0
+    d["h0"].zero_()
+    d["dhT"].zero_()
+    return d
+
+
+@gpu
+@pytest.mark.parametrize("B,T,D,N", CUTS)
+def test_scan_gates_that_grow(B, T, D, N):
+    """The product of a run of gates overflows where nothing that it multiplies does."""
+    say("scan growing gates", (B, T, D, N))
+    d = _growing(B, T, D, N, F32)
+    (y, hT, _), got = run_scan(d, F32, softplus=False)
+    rin = [d[k] for k in NAMES]
+    ry, rh, _, _ = R.scan_fwd(*rin, softplus=False)
+    sy, sh, _, _ = R.scan_fwd(*rin, softplus=False, absolute=True)
+    # a gate's argument is near 30 (43 as a power of two): its two roundings count that often, for two gates
+    c = 4 * 2 + 40 + N + 2 * 2 * 44
+    e = {"y": R.worst(y, ry, sy, F32, c), "hT": R.worst(hT, rh, sh, F32, c)}
+    ref = R.scan_bwd(*rin[:5], d["dy"], d["dhT"], *rin[5:], softplus=False)
+    sc = R.scan_bwd(*rin[:5], d["dy"], d["dhT"], *rin[5:], softplus=False, absolute=True)
+    # dBm and dCm add up the channels, dA the steps (two of them are not zero) of all sequences
+    extra = dict(A=2 * B, Bm=D, Cm=D)
+    for name, gt, r, s in zip(NAMES, got, ref, sc):
+        if gt is not None:
+            e["d" + name] = R.worst(gt, r, s, F32, 2 * c + 40 + extra.get(name, 0))
+    print(e, flush=True)
+    assert max(e.values()) <= 1.0, e
+
+
+def check_grown(d, argument):
+    """Forward against the reference where gates only multiply a carried state: each
+    rounding of a gate's argument counts |argument| (as a power of two), twice a step."""
+    (y, hT, _), _ = run_scan(d, F32, softplus=False, backward=False)
+    rin = [d[k] for k in NAMES]
+    ry, rh, _, _ = R.scan_fwd(*rin, softplus=False)
+    sy, sh, _, _ = R.scan_fwd(*rin, softplus=False, absolute=True)
+    T, N = d["u"].shape[1], d["A"].shape[1]
+    c = 4 * T + 40 + N + 2 * T * argument
+    e = {"y": R.worst(y, ry, sy, F32, c), "hT": R.worst(hT, rh, sh, F32, c)}
+    print(e, flush=True)
+    assert max(e.values()) <= 1.0, e
+
+
+@gpu
+@pytest.mark.parametrize("N", [1, 6, 16, 20, 40])
+def test_scan_small_state_that_grows(N):
+    """A state of 2^-100 under 16 gates of e^9: the product is 2^207, the state ends at 2^107."""
+    say("scan small growing state", N)
+    d = scan_inputs(2, 16, 24, 1, N, F32, N, skip=False, z=False, bias=False)
+    d["delta"], d["A"] = torch.full_like(d["delta"], 0.5), torch.full_like(d["A"], 18.0)
+    d["u"].zero_()
+    d["h0"] = quant(torch.sign(d["h0"]) * 2.0 ** -100, F32)
+    check_grown(d, 13)
+
+
+@gpu
+def test_scan_segments_that_grow_and_shrink():
+    """Segments of 512 steps over which the state grows by 2^216 and shrinks again."""
+    say("scan segments that grow and shrink, B=1 T=4096 D=3056 N=1")
+    T, D = 4096, 3056
+    d = scan_inputs(1, T, D, 1, 1, F32, 5, skip=False, z=False, bias=False)
+    d["A"] = torch.full_like(d["A"], 1.0)
+    up = (torch.arange(T) // 256 % 2 == 0).double() * 2 - 1
+    d["delta"] = quant((up * 0.5859375)[None, :, None].expand(1, T, D), F32)
+    d["u"].zero_()
+    d["h0"] = quant(torch.sign(d["h0"]) * 2.0 ** -120, F32)
+    assert lrs.mi_selective_scan_fwd_workspace(1, T, D, 1, 1) == 2 * 8 * D * 4  # eight segments
+    check_grown(d, 1)
