@@ -62,7 +62,7 @@ __global__ __launch_bounds__(NW * 64, WPS) void scan_fwd_kernel(ScanArgs p) {
 #pragma unroll
         for (int s = 0; s < S; ++s) {
             const int n = sg * S + s;
-            A2[s][c] = ok && n < p.N ? p.A[d * p.N + n] * LOG2E : 0.f;
+            A2[s][c] = ok && n < p.N ? gate_base(p.A[d * p.N + n]) : 0.f;
         }
     }
     // folded states: thread tid carries positions tid, tid + NT, ... of the tile
@@ -250,7 +250,7 @@ __global__ __launch_bounds__(NW * 64, WPS) void scan_fwd_kernel(ScanArgs p) {
                         int ln, e;
                         LV::where(i, &ln, &e);
                         const int n = (ln >> 4) * S + e % S, q = e / S;
-                        const float a2 = st_off[f] >= 0 ? p.A[d0 * p.N + st_off[f]] * LOG2E : 0.f;
+                        const float a2 = st_off[f] >= 0 ? gate_base(p.A[d0 * p.N + st_off[f]]) : 0.f;
                         c = carry[f];
 #pragma unroll 1
                         for (int w = 0; w < NW; ++w) {
@@ -378,7 +378,7 @@ __global__ __launch_bounds__(256) void scan_step_kernel(ScanArgs p, int wg_row) 
     float acc = 0.f;
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-        h[s] = fmaf(__builtin_amdgcn_exp2f(dl * (A[s] * LOG2E)), h[s], dl * uu * Bv[s]);
+        h[s] = fmaf(__builtin_amdgcn_exp2f(dl * gate_base(A[s])), h[s], dl * uu * Bv[s]);
         acc = fmaf(Cv[s], h[s], acc);
     }
     float *ho = p.hT + chan * N + n0;

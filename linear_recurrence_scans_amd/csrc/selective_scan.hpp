@@ -212,6 +212,14 @@ __device__ __forceinline__ float gate_rate(float raw, int use_softplus, float *d
     return raw;
 }
 
+// A log2(e), the factor of a gate's exponent.  It is kept finite (a NaN stays one), so
+// that a rate of zero, which is also what a step that does not exist has, makes a gate
+// of one for A = -inf too.
+__device__ __forceinline__ float gate_base(float A) {
+    const float a = A * LOG2E;
+    return a < -__FLT_MAX__ ? -__FLT_MAX__ : a;
+}
+
 // LDS ordering.  Fences of the local address space make the compiler and the
 // LDS queue keep the order without waiting for global loads in flight, which a
 // __syncthreads() would drain.  wave_lds_sync: data exchanged inside one wave;

@@ -119,7 +119,7 @@ __global__ __launch_bounds__(NW * 64) void scan_bwd_sum_kernel(ScanArgs p) {
 #pragma unroll
         for (int s = 0; s < S; ++s) {
             const int n = sg * S + s;
-            A2[s][c] = c < nv && n < p.N ? p.A[d * p.N + n] * LOG2E : 0.f;
+            A2[s][c] = c < nv && n < p.N ? gate_base(p.A[d * p.N + n]) : 0.f;
         }
     }
     float edge[FPT], prod[FPT];
@@ -277,7 +277,7 @@ __global__ __launch_bounds__(NW * 64, 2) void scan_bwd_kernel(ScanArgs p) {
 #pragma unroll
         for (int s = 0; s < S; ++s) {
             const int n = sg * S + s;
-            A2[s][c] = ok && n < p.N ? p.A[d * p.N + n] * LOG2E : 0.f;
+            A2[s][c] = ok && n < p.N ? gate_base(p.A[d * p.N + n]) : 0.f;
             dA[s][c] = 0.f;
         }
     }

@@ -111,3 +111,48 @@ def test_scan_segments_that_grow_and_shrink():
     d["h0"] = quant(torch.sign(d["h0"]) * 2.0 ** -120, F32)
     assert lrs.mi_selective_scan_fwd_workspace(1, T, D, 1, 1) == 2 * 8 * D * 4  # eight segments
     check_grown(d, 1)
+
+
+@gpu
+@pytest.mark.parametrize("N", [1, 6, 16, 20, 40])
+@pytest.mark.parametrize("T,lengths", [(5, None), (150, [150, 0, 33])])
+def test_scan_rates_that_forget_everything(T, lengths, N):
+    """A of -inf: a gate is zero wherever the rate is not, also in a block whose last
+    steps do not exist.  A of -3e38, finite, has gradients too."""
+    say("scan A = -inf and -3e38", T, N, lengths)
+    d = scan_inputs(3, T, 24, 1, N, F32, T + N, lengths=lengths)
+    for low, backward in ((float("-inf"), False), (-3e38, True)):
+        d["A"][:, 0] = low
+        d["A"] = quant(d["A"], F32)
+        (y, hT, _), got = run_scan(d, F32, lengths=lengths, backward=backward)
+        rin = [d[k] for k in NAMES]
+        ry, rh, _, _ = R.scan_fwd(*rin, lengths=d["lengths"])
+        sy, sh, _, _ = R.scan_fwd(*rin, lengths=d["lengths"], absolute=True)
+        c = 4 * T + 40 + N
+        e = {"y": R.worst(y, ry, sy, F32, c), "hT": R.worst(hT, rh, sh, F32, c)}
+        if backward:
+            ref = R.scan_bwd(*rin[:5], d["dy"], d["dhT"], *rin[5:], lengths=d["lengths"])
+            sc = R.scan_bwd(*rin[:5], d["dy"], d["dhT"], *rin[5:], lengths=d["lengths"], absolute=True)
+            extra = dict(A=3 * T, Bm=24, Cm=24, skip=3 * T, delta_bias=3 * T)
+            for name, gt, r, s in zip(NAMES, got, ref, sc):
+                e["d" + name] = R.worst(gt, r, s, F32, 2 * c + 40 + extra.get(name, 0))
+        print(e, flush=True)
+        assert max(e.values()) <= 1.0, e
+
+
+@gpu
+def test_scan_step_that_forgets_everything():
+    """The single-token step with A of -3e38: a rate of zero keeps the state, any other replaces it."""
+    say("scan step A = -3e38")
+    d = scan_inputs(2, 1, 24, 1, 16, F32, 3)
+    d["A"][:, 3] = quant(torch.tensor(-3e38, dtype=torch.float64), F32)
+    d["delta"][0] = -200.0
+    t = {k: dev(v, F32) for k, v in d.items() if v is not None}
+    y, h = lrs.mi_selective_scan_step(t["u"][:, 0], t["delta"][:, 0], t["A"], t["Bm"][:, 0], t["Cm"][:, 0], t["h0"],
+                                      t["skip"], t["z"][:, 0], t["delta_bias"])
+    rin = [d[k] for k in NAMES]
+    ry, rh, _, _ = R.scan_fwd(*rin)
+    sy, sh, _, _ = R.scan_fwd(*rin, absolute=True)
+    e = {"y": R.worst(y, ry[:, 0], sy[:, 0], F32, 60), "h": R.worst(h, rh, sh, F32, 60)}
+    print(e, flush=True)
+    assert max(e.values()) <= 1.0, e
