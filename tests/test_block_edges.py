@@ -156,3 +156,51 @@ def test_scan_step_that_forgets_everything():
     e = {"y": R.worst(y, ry[:, 0], sy[:, 0], F32, 60), "h": R.worst(h, rh, sh, F32, 60)}
     print(e, flush=True)
     assert max(e.values()) <= 1.0, e
+
+
+# ---------------------------------------------------------------------------
+# the rate softplus(x)
+# ---------------------------------------------------------------------------
+
+@gpu
+def test_rate_is_accurate_relative_to_itself():
+    """One state, A = 0 and ones elsewhere: y is the rate, ddelta its derivative.  The rate's
+    bound, in half steps of 2^-24: two for each of exp2 and log2, one each for the product's
+    remainder, the join and the sum with max(x, 0), one for the remainder of 1 + e taken
+    without its factor 1 / (1 + e); and ln 2 in fp32 leaves 0.05 |x| of the remainder.  The
+    derivative's: exp2 and its remainder as there, two for the reciprocal, one each for
+    1 + e and the products.  Rates of 1e-3 to 1e-1 lie at x = -7 to -2."""
+    say("softplus rates")
+    x = torch.cat([torch.linspace(-80, 80, 8192, dtype=torch.float64), torch.linspace(-16, 4, 16384, dtype=torch.float64),
+                   torch.tensor([0.0, -1e-30, 1e-30, 500.0], dtype=torch.float64)]).float().double()
+    n = x.numel()
+    want = torch.clamp(x, min=0) + torch.log1p(torch.exp(-x.abs()))
+    one = torch.ones(1, 1, 1, 1, device="cuda")
+    u, A = torch.ones(1, 1, n, device="cuda"), torch.zeros(n, 1, device="cuda")
+    delta = x.float().cuda().view(1, 1, n)
+    y, hT, st = lrs.mi_selective_scan_fwd(u, delta, A, one, one, save_states=True)
+    dd = lrs.mi_selective_scan_bwd(u, delta, A, one, one, st, torch.ones_like(u))[1]
+    y1, h1 = lrs.mi_selective_scan_step(u[:, 0], delta[:, 0], A, one[:, 0], one[:, 0], torch.zeros(1, n, 1, device="cuda"))
+    lim = (8 + 0.05 * x.abs()) * 2.0 ** -24 * want
+    worst = {k: float(((g.cpu().double().view(-1) - want).abs() / lim).max())
+             for k, g in (("y", y), ("hT", hT), ("y1", y1), ("h1", h1))}
+    der = torch.exp(-torch.log1p(torch.exp(-x)))
+    worst["ddelta"] = float(((dd.cpu().double().view(-1) - der).abs() / ((8 + 0.05 * x.abs()) * 2.0 ** -24 * der)).max())
+    print(worst, flush=True)
+    assert max(worst.values()) <= 1.0, worst
+
+
+@gpu
+def test_rate_of_infinities():
+    """softplus(-inf) is zero (the state stays, the token leaves no trace); inf and NaN stay
+    what they are in the state, and y is not finite either."""
+    say("softplus of -inf, inf, NaN")
+    x = torch.tensor([float("-inf"), -1000.0, 1000.0, float("inf"), float("nan")], device="cuda")
+    one = torch.ones(1, 1, 1, 1, device="cuda")
+    h0 = torch.full((1, 5, 1), 3.0, device="cuda")
+    y, hT, _ = lrs.mi_selective_scan_fwd(torch.ones(1, 1, 5, device="cuda"), x.view(1, 1, 5),
+                                         torch.full((5, 1), -1.0, device="cuda"), one, one, h0=h0)
+    y, hT = y.flatten().tolist(), hT.flatten().tolist()
+    assert y[:3] == hT[:3] == [3.0, 3.0, 1000.0]
+    assert hT[3] == float("inf") and hT[4] != hT[4]
+    assert not torch.isfinite(torch.tensor(y[3:])).any()
