@@ -241,6 +241,9 @@ mi_status mi_affine_scan_bwd_h0(const void *A, const void *Abar, const void *H, 
 /* NULL for T each) gives every sequence its own length; values are clamped */
 /* to [0, T].  Steps at or past it are not read into any result (they may   */
 /* hold anything, NaN included); outputs and gradients there are zero.      */
+/*                                                                          */
+/* A launch holds fewer than 2^32 threads: a call that needs more, such as  */
+/* the scan's backward for 2^23 sequences, is MI_ERR_UNSUPPORTED.           */
 /* ------------------------------------------------------------------------ */
 
 typedef enum {

@@ -327,8 +327,6 @@ int64_t time_tiles(int64_t T, int64_t rows) {
     return n < 1 ? 1 : n;  // an empty sequence still writes its state
 }
 
-constexpr int64_t MAX_GRID = 0x7fffffff;
-
 struct ConvSizes {
     int64_t x, taps, bias, state;  // bytes
 };
@@ -374,7 +372,7 @@ mi_status mi_causal_conv_fwd(const void *x, const float *w, const float *bias, c
     const int64_t tile = 64 * vec;
     const int64_t n_dt = (D + tile - 1) / tile, n_tt = time_tiles(T, CONV_NW * CONV_FWD_R);
     int64_t grid;
-    if (!mul_ok(B, n_dt, n_tt, 1, &grid) || grid > MAX_GRID) return MI_ERR_UNSUPPORTED;
+    if (!mul_ok(B, n_dt, n_tt, 1, &grid) || !launch_fits(grid, CONV_NW * 64)) return MI_ERR_UNSUPPORTED;
     a.n_dt = (int)n_dt; a.n_tt = (int)n_tt;
     return with_type(dt, K, [&](auto tag, auto num) {
         using T_ = typename decltype(tag)::type;
@@ -437,7 +435,7 @@ mi_status mi_causal_conv_bwd(const void *x, const float *w, const float *bias, c
         const int64_t tile = 64 * vec;
         const int64_t n_dt = (D + tile - 1) / tile;
         int64_t grid;
-        if (!mul_ok(B, n_dt, n_tt, 1, &grid) || grid > MAX_GRID) return MI_ERR_UNSUPPORTED;
+        if (!mul_ok(B, n_dt, n_tt, 1, &grid) || !launch_fits(grid, CONV_NW * 64)) return MI_ERR_UNSUPPORTED;
         a.n_dt = (int)n_dt; a.n_tt = (int)n_tt;
         st = with_type(dt, K, [&](auto tag, auto num) {
             using T_ = typename decltype(tag)::type;
@@ -475,7 +473,7 @@ mi_status mi_causal_conv_step(const void *x, const float *w, const float *bias, 
     a.x = x; a.w = w; a.bias = bias; a.x0 = x0; a.y = y; a.xT = x_out; a.T = 1; a.D = D; a.act = act;
     const int64_t n = B * D / vec;
     const int64_t grid = (n + 255) / 256;
-    if (grid > MAX_GRID) return MI_ERR_UNSUPPORTED;
+    if (!launch_fits(grid, 256)) return MI_ERR_UNSUPPORTED;
     return with_type(dt, K, [&](auto tag, auto num) {
         using T_ = typename decltype(tag)::type;
         constexpr int K_ = decltype(num)::value, V = (int)(8 / sizeof(T_));

@@ -23,6 +23,9 @@ inline bool mul_ok(int64_t a, int64_t b, int64_t c, int64_t d, int64_t *out) {
     return true;
 }
 
+// Whether one launch can hold `groups` workgroups: a grid counts its threads in 32 bits.
+inline bool launch_fits(int64_t groups, int64_t threads) { return groups <= (int64_t)0xffffffffll / threads; }
+
 struct Buf {
     const void *p;
     int64_t bytes;

@@ -420,7 +420,7 @@ template <typename T, bool BWD>
 mi_status run_norm(NormArgs a, int vec, hipStream_t s, int64_t *parts) {
     const NormPlan q = norm_plan(a.R, a.D, a.G, vec, BWD);
     int64_t grid;
-    if (!mul_ok(q.slices, q.parts, 1, 1, &grid) || grid > 0x7fffffff) return MI_ERR_UNSUPPORTED;
+    if (!mul_ok(q.slices, q.parts, 1, 1, &grid) || !launch_fits(grid, 256)) return MI_ERR_UNSUPPORTED;
     a.rows = q.rows;
     a.gps = norm_gps(q, a.G);
     a.n_slices = (int)q.slices;

@@ -402,7 +402,7 @@ template <typename T, int LQ>
 mi_status launch_step(const ScanArgs &a, bool quad, hipStream_t s) {
     const int64_t wg_row = (a.D + 256 / LQ - 1) / (256 / LQ);
     int64_t grid;
-    if (!mul_ok(a.B, wg_row, 1, 1, &grid) || grid > 0x7fffffff) return MI_ERR_UNSUPPORTED;
+    if (!mul_ok(a.B, wg_row, 1, 1, &grid) || !launch_fits(grid, 256)) return MI_ERR_UNSUPPORTED;
     const dim3 gd((unsigned)grid), bd(256);
     if (quad) hipLaunchKernelGGL((scan_step_kernel<T, LQ, true>), gd, bd, 0, s, a, (int)wg_row);
     else hipLaunchKernelGGL((scan_step_kernel<T, LQ, false>), gd, bd, 0, s, a, (int)wg_row);
@@ -424,7 +424,7 @@ template <typename T, int S, int C, int L, int NW, int WPS, bool CUT>
 mi_status launch_tile(ScanArgs a, int64_t n_seg, hipStream_t s) {
     a.tiles = (a.per + 16 * C - 1) / (16 * C);
     int64_t items;
-    if (!mul_ok(a.B, a.G, a.tiles, n_seg, &items) || items > 0x7ffffff0) return MI_ERR_UNSUPPORTED;
+    if (!mul_ok(a.B, a.G, a.tiles, n_seg, &items) || !launch_fits(items + 7, NW * 64)) return MI_ERR_UNSUPPORTED;
     a.n_seg = (int)n_seg;
     a.seg = (a.T + NW * L * n_seg - 1) / (NW * L * n_seg) * (NW * L);
     if constexpr (CUT)

@@ -703,7 +703,7 @@ mi_status launch_bwd(ScanArgs a, hipStream_t s) {
     a.tiles = (int)bwd_tiles(a.per, a.N);
     a.seg = (a.T + BLK * a.n_seg - 1) / (BLK * a.n_seg) * BLK;
     int64_t items;
-    if (!mul_ok(a.B, a.G, a.tiles, a.n_seg, &items) || items > 0x7ffffff0) return MI_ERR_UNSUPPORTED;
+    if (!mul_ok(a.B, a.G, a.tiles, a.n_seg, &items) || !launch_fits(items + 7, TL::NW * 64)) return MI_ERR_UNSUPPORTED;
     if (a.n_seg > 1) {
         a.n_items = (int)(items / a.n_seg * (a.n_seg - 1));
         hipLaunchKernelGGL((scan_bwd_sum_kernel<T, S, TL::C, TL::L, TL::NW>), dim3(xcd_grid(a.n_items)),

@@ -204,3 +204,28 @@ def test_rate_of_infinities():
     assert y[:3] == hT[:3] == [3.0, 3.0, 1000.0]
     assert hT[3] == float("inf") and hT[4] != hT[4]
     assert not torch.isfinite(torch.tensor(y[3:])).any()
+
+
+# ---------------------------------------------------------------------------
+# limits of a launch (CPU: nothing is launched, the addresses are never read)
+# ---------------------------------------------------------------------------
+
+def test_calls_beyond_one_launch_are_refused():
+    """2^32 threads or more: refused as unsupported before any launch."""
+    L = lrs._load()
+    UNSUPPORTED = 2
+    p = [(1 << 42) * (i + 1) for i in range(22)]
+    far = 1 << 60
+    assert L.mi_causal_conv_fwd(p[0], p[1], None, None, None, p[2], None, 1 << 24, 1, 4, 4, 0, 0, None) == UNSUPPORTED
+    assert L.mi_causal_conv_bwd(p[0], p[1], None, None, None, p[2], None, p[3], p[4], None, None, 1 << 24, 1, 4, 4, 0, 0,
+                                far, 1 << 50, None) == UNSUPPORTED
+    assert L.mi_causal_conv_step(p[0], p[1], None, p[2], p[3], p[4], 1 << 32, 1, 2, 0, 0, None) == UNSUPPORTED
+    assert L.mi_selective_scan_fwd(*p[:5], None, None, None, None, None, p[5], p[6], None, 1 << 24, 1, 1, 1, 1, 1, 0,
+                                   None, 0, None) == UNSUPPORTED
+    assert L.mi_selective_scan_bwd(*p[:5], None, None, None, p[5], None, p[6], None, *p[7:12], None, None, None, None,
+                                   1 << 23, 1, 1, 1, 1, 1, 0, far, 1 << 50, None) == UNSUPPORTED
+    assert L.mi_selective_scan_step(*p[:6], None, None, None, p[6], p[7], 1 << 24, 1, 1, 1, 1, 0, None) == UNSUPPORTED
+    G = 1 << 24
+    assert L.mi_group_norm_fwd(p[0], None, None, None, p[1], 1, 260 * G, G, 1e-5, 1, 0, 0, None) == UNSUPPORTED
+    assert L.mi_group_norm_bwd(p[0], None, None, None, p[1], p[2], None, None, None, 1, 260 * G, G, 1e-5, 1, 0, 0, far,
+                               1 << 50, None) == UNSUPPORTED
