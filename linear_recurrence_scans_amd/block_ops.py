@@ -89,6 +89,8 @@ def _new(t, like: torch.Tensor, shape, name: str, dtype=None):
     """An output: the caller's `t`, checked, or a new tensor."""
     if t is None:
         return torch.empty(shape, dtype=dtype or like.dtype, device=like.device)
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
     if t.shape != shape or t.dtype != (dtype or like.dtype) or t.device != like.device or not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s tensor of shape %s on %s"
                          % (name, dtype or like.dtype, tuple(shape), like.device))

@@ -229,3 +229,18 @@ def test_calls_beyond_one_launch_are_refused():
     assert L.mi_group_norm_fwd(p[0], None, None, None, p[1], 1, 260 * G, G, 1e-5, 1, 0, 0, None) == UNSUPPORTED
     assert L.mi_group_norm_bwd(p[0], None, None, None, p[1], p[2], None, None, None, 1, 260 * G, G, 1e-5, 1, 0, 0, far,
                                1 << 50, None) == UNSUPPORTED
+
+
+def test_outputs_that_are_no_tensors():
+    """An output given by the caller is checked for what it is before its shape is."""
+    from linear_recurrence_scans_amd import block_ops
+    like = torch.zeros(2, 3)
+    for bad in ([0.0] * 6, 1, "y"):
+        with pytest.raises(TypeError, match="y must be a torch.Tensor"):
+            block_ops._new(bad, like, (2, 3), "y")
+        with pytest.raises(TypeError, match="y must be a torch.Tensor"):
+            block_ops._out(bad, like, "y")
+    with pytest.raises(ValueError, match="y must be a contiguous"):
+        block_ops._new(torch.zeros(3, 2).t(), like, (2, 3), "y")
+    ok = torch.zeros(2, 3)
+    assert block_ops._out(ok, like, "y") is ok
