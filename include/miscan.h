@@ -292,7 +292,14 @@ mi_status mi_causal_conv_step(const void *x, const float *w, const float *bias, 
  * the backward needs: the fp32 state before every block of
  * mi_selective_scan_block(N) steps, (B, ceil(T/block), D, N).  The workspace
  * holds the transforms of a sequence's segments where the channels alone do
- * not fill the GPU; it may be NULL where the query says 0 bytes. */
+ * not fill the GPU; it may be NULL where the query says 0 bytes.
+ *
+ * Non-finite values.  A result that the formulas make infinite may be NaN
+ * instead (steps are composed, and inf 0 arises where one step after the other
+ * would keep the infinity); a result that does not depend on a non-finite input
+ * is not touched by it.  Rates of growth (exp(dl A) > 1) are finite in the
+ * results as long as every gate, state and gradient is.  A may be -inf: such a
+ * state keeps its value over steps of rate zero and forgets it over any other. */
 int64_t mi_selective_scan_block(int64_t N);
 size_t mi_selective_scan_fwd_workspace(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N, mi_dtype dt);
 mi_status mi_selective_scan_fwd(const void *u, const void *delta, const float *A, const void *Bm,

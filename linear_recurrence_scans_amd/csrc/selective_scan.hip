@@ -245,8 +245,10 @@ __global__ __launch_bounds__(NW * 64, WPS) void scan_fwd_kernel(ScanArgs p) {
                         enter(w, c);
                         c = fmaf(pw[w], c, sv[w]);
                     }
-                    // a product out of range: step by step
-                    if (__builtin_expect(!__builtin_isfinite(c), 0)) {
+                    // a product out of range: step by step, from the first wave that a value
+                    // which is not finite enters (so do all after it)
+                    const bool bad = !__builtin_isfinite(c);
+                    if (__builtin_expect(__any(bad), 0) && bad) {
                         int ln, e;
                         LV::where(i, &ln, &e);
                         const int n = (ln >> 4) * S + e % S, q = e / S;
@@ -254,7 +256,9 @@ __global__ __launch_bounds__(NW * 64, WPS) void scan_fwd_kernel(ScanArgs p) {
                         c = carry[f];
 #pragma unroll 1
                         for (int w = 0; w < NW; ++w) {
-                            enter(w, c);
+                            const float v = sm_s[w][i];
+                            if (__builtin_isfinite(v)) c = v;
+                            else enter(w, c);
 #pragma unroll 1
                             for (int t = 0; t < L; ++t) {
                                 const float *x = sm_x[w][t][ln & 15];

@@ -7,7 +7,7 @@ import torch
 
 import block_ref as R
 import linear_recurrence_scans_amd as lrs
-from test_block_ops import BF16, F16, F32, NAMES, dev, quant, say, scan_inputs
+from test_block_ops import F32, NAMES, dev, quant, say, scan_inputs
 
 gpu = pytest.mark.gpu
 
@@ -244,3 +244,48 @@ def test_outputs_that_are_no_tensors():
         block_ops._new(torch.zeros(3, 2).t(), like, (2, 3), "y")
     ok = torch.zeros(2, 3)
     assert block_ops._out(ok, like, "y") is ok
+
+
+# ---------------------------------------------------------------------------
+# non-finite inputs
+# ---------------------------------------------------------------------------
+
+@gpu
+@pytest.mark.parametrize("what,value", [("u", float("inf")), ("u", float("nan")), ("delta", float("inf"))])
+@pytest.mark.parametrize("B,T,D,N", [(2, 300, 16, 6), (4, 70, 800, 16), (16, 40, 1280, 16), (2, 70, 16, 40)])
+def test_scan_nonfinite_inputs_stay_in_their_channel(B, T, D, N, what, value):
+    """One bad token of one channel: what the formulas do not make of it keeps its bits, and
+    what they do is not finite."""
+    say("scan with", what, value, (B, T, D, N))
+    b, t, c = 1, 21, 5
+    d = scan_inputs(B, T, D, 1, N, F32, N)
+    (y, hT, st), g = run_scan(d, F32)
+    d[what][b, t, c] = value
+    (y2, hT2, st2), g2 = run_scan(d, F32)
+    seen = torch.zeros(B, T, D, dtype=torch.bool, device="cuda")
+    seen[b, t:, c] = True
+    assert torch.equal(y[~seen], y2[~seen]) and not torch.isfinite(y2[seen]).any()
+    own = torch.zeros(B, D, dtype=torch.bool, device="cuda")
+    own[b, c] = True
+    assert torch.equal(hT[~own], hT2[~own]) and not torch.isfinite(hT2[own]).any()
+    same = lambda i, keep: torch.equal(g[i][keep], g2[i][keep])
+    for i, name in enumerate(NAMES):
+        if name in ("u", "delta", "z"):
+            keep = torch.ones(B, T, D, dtype=torch.bool, device="cuda")
+            keep[b, :, c] = False
+        elif name in ("Bm", "Cm"):  # sums over the channels
+            keep = torch.ones(B, T, dtype=torch.bool, device="cuda")
+            keep[b] = False
+            if name == "Cm":
+                keep[b, :t] = True  # the states before
+            elif what == "u":
+                keep[b] = True      # g of the other tokens does not depend on u
+                keep[b, t] = False
+        elif name == "h0":
+            keep = ~own
+        else:
+            keep = torch.ones(D, dtype=torch.bool, device="cuda")
+            keep[c] = False
+        assert same(i, keep), name
+    if what == "u":  # neither du nor dh0 depends on u
+        assert same(0, slice(None)) and same(8, slice(None))
