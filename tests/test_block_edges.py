@@ -7,7 +7,8 @@ import torch
 
 import block_ref as R
 import linear_recurrence_scans_amd as lrs
-from test_block_ops import F32, NAMES, dev, quant, say, scan_inputs
+from test_block_ops import (BF16, F16, F32, NAMES, check_scan, conv_inputs, dev, poison, quant, say,
+                            scan_inputs)
 
 gpu = pytest.mark.gpu
 
@@ -289,3 +290,92 @@ def test_scan_nonfinite_inputs_stay_in_their_channel(B, T, D, N, what, value):
         assert same(i, keep), name
     if what == "u":  # neither du nor dh0 depends on u
         assert same(0, slice(None)) and same(8, slice(None))
+
+
+# ---------------------------------------------------------------------------
+# every way a call is cut, over several blocks and turns
+# ---------------------------------------------------------------------------
+
+@gpu
+@pytest.mark.parametrize("T,N,dtype", [(600, 3, F32), (600, 4, F16), (300, 7, F32), (300, 8, BF16), (300, 16, F32),
+                                       (300, 16, BF16), (300, 16, F16), (200, 24, BF16), (110, 33, F32), (110, 64, F16)])
+def test_scan_narrow_tiles_over_several_blocks(T, N, dtype):
+    """Narrow tiles of the forward, at least three blocks of 32 to 256 steps, each number of
+    states a lane holds; the states it saves; the backward in segments and without."""
+    check_scan(4, T, 800, 1, N, dtype, T + N, lengths=[T, 0, T // 2 + 3, 1])
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("B,T,D,G,N,lengths", [(1, 1000, 16, 1, 16, None), (2, 700, 24, 1, 4, [700, 333]),
+                                               (1, 650, 40, 2, 6, None), (2, 500, 20, 1, 40, [0, 257]),
+                                               (1, 600, 31, 1, 20, None), (16, 40, 1280, 1, 8, None)])
+def test_scan_cuts_in_16_bits(B, T, D, G, N, lengths, dtype):
+    """Segments of both directions and wide tiles."""
+    check_scan(B, T, D, G, N, dtype, T + D, lengths=lengths)
+
+
+def conv_all(d, act, absolute=False):
+    """R.conv_fwd and R.conv_bwd with all steps at once: y, xT, dx, dw, dbias, dx0."""
+    ab = (lambda t: t.abs()) if absolute else (lambda t: t)
+    x, w, K, ln = d["x"], d["w"], d["w"].shape[1], d["lengths"].long()
+    B, T, D = x.shape
+    ok = (torch.arange(T)[None] < ln[:, None])[..., None]
+    xe = torch.cat([d["x0"], torch.where(ok, x, 0.0)], 1)
+    rows = ln[:, None] + torch.arange(K - 1)[None]
+    pick = rows[..., None].expand(B, K - 1, D)
+    win = lambda e, k: e[:, k:k + T]
+    s = d["bias"] + sum(win(xe, k) * w[:, k] for k in range(K))
+    mag = sum(win(xe, k).abs() * w[:, k].abs() for k in range(K))
+    sa = mag + d["bias"].abs() if absolute else s
+    y = (sa * 1.1 if absolute else R.silu(s)) if act else sa
+    ds = ab(d["dy"])
+    if act:
+        ds = ds * (1.1 + 0.5 * mag if absolute else R.dsilu(s))
+    ds = torch.where(ok, ds, 0.0)
+    dxe = torch.zeros_like(xe)
+    for k in range(K):
+        dxe[:, k:k + T] += ds * ab(w)[:, k]
+    dxe.scatter_add_(1, pick, ab(d["dxT"]))
+    dw = torch.stack([(ds * win(ab(xe), k)).sum((0, 1)) for k in range(K)], 1)
+    return (torch.where(ok, y, 0.0), torch.gather(xe, 1, pick), torch.where(ok, dxe[:, K - 1:], 0.0), dw,
+            ds.sum((0, 1)), dxe[:, :K - 1])
+
+
+@pytest.mark.parametrize("absolute", [False, True])
+@pytest.mark.parametrize("act", [None, "silu"])
+@pytest.mark.parametrize("K", [2, 4])
+def test_conv_all_is_the_reference(K, act, absolute):
+    d = conv_inputs(3, 7, 4, K, F32, K, lengths=[7, 0, 2])
+    args = (d["x"], d["w"], d["bias"], d["x0"])
+    want = R.conv_fwd(*args, d["lengths"], act, absolute)[:1] + \
+        R.conv_fwd(*args, d["lengths"], act)[1:] + \
+        R.conv_bwd(*args, d["dy"], d["dxT"], d["lengths"], act, absolute)
+    for name, g, r in zip(("y", "xT", "dx", "dw", "dbias", "dx0"), conv_all(d, act, absolute), want):
+        assert float((g - r).abs().max()) <= 1e-12, name
+
+
+@gpu
+@pytest.mark.parametrize("B,T,D,K,dtype,run", [(1400, 70, 12, 4, BF16, 32), (2100, 70, 10, 3, F32, 64),
+                                               (900, 300, 8, 5, F16, 64), (1400, 70, 9, 4, F32, 32)])
+def test_conv_backward_long_runs(B, T, D, K, dtype, run):
+    """Runs of 32 and 64 steps a wave (shorter ones are all that few sequences get), lengths
+    that end inside them."""
+    say("conv backward, runs of", run, (B, T, D, K), dtype)
+    g = torch.Generator().manual_seed(B)
+    d = conv_inputs(B, T, D, K, dtype, K, lengths=torch.randint(0, T + 1, (B,), generator=g).tolist())
+    ln, lnd = d["lengths"], d["lengths"].cuda()
+    # the partial rows that the workspace holds tell the run: four waves a workgroup
+    rows = lrs.mi_causal_conv_bwd_workspace(B, T, D, K, dtype) // ((K + 1) * D * 4)
+    assert rows == B * -(-T // (4 * run))
+    x, dy = dev(poison(d["x"], ln), dtype), dev(poison(d["dy"], ln), dtype)
+    w, bias, x0, dxT = dev(d["w"], F32), dev(d["bias"], F32), dev(d["x0"], dtype), dev(d["dxT"], dtype)
+    y, xT = lrs.mi_causal_conv_fwd(x, w, bias, x0, act="silu", lengths=lnd)
+    got = (y, xT) + tuple(lrs.mi_causal_conv_bwd(x, w, bias, x0, dy, dxT, act="silu", lengths=lnd))
+    ref, sc = conv_all(d, "silu"), conv_all(d, "silu", absolute=True)
+    e, c = {}, 2 * K + 26
+    for name, gt, r, s, ty, n in zip(("y", "xT", "dx", "dw", "dbias", "dx0"), got, ref, sc,
+                                     (dtype, dtype, dtype, F32, F32, dtype), (K + 13, 0, c, c + B * T, c + B * T, c)):
+        e[name] = R.worst(gt, r, s, ty, n)
+    print(e, flush=True)
+    assert torch.equal(xT.cpu().double(), ref[1]) and max(e.values()) <= 1.0, e
