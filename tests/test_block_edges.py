@@ -7,7 +7,7 @@ import torch
 
 import block_ref as R
 import linear_recurrence_scans_amd as lrs
-from test_block_ops import (BF16, F16, F32, NAMES, check_scan, conv_inputs, dev, poison, quant, say,
+from test_block_ops import (BF16, F16, F32, NAMES, check_norm, check_scan, conv_inputs, dev, poison, quant, say,
                             scan_inputs)
 
 gpu = pytest.mark.gpu
@@ -379,3 +379,15 @@ def test_conv_backward_long_runs(B, T, D, K, dtype, run):
         e[name] = R.worst(gt, r, s, ty, n)
     print(e, flush=True)
     assert torch.equal(xT.cpu().double(), ref[1]) and max(e.values()) <= 1.0, e
+
+
+@gpu
+@pytest.mark.parametrize("rows,D,G,dtype", [(1100, 515, 1, F32), (4099, 515, 1, F16), (1100, 264, 1, BF16),
+                                            (4099, 64, 1, F32), (4099, 64, 4, F16), (40003, 64, 1, BF16),
+                                            (1031, 4097, 1, F32), (2061, 4097, 1, BF16), (9001, 24, 24, F32),
+                                            (1027, 6144, 1, BF16), (1030, 10240, 2, F16)])
+def test_norm_workgroups_walk_several_rows(rows, D, G, dtype):
+    """More rows than workgroups take at once, in each kind of team and in the kernel for any
+    width: parameters' gradients add up over the turns, and the last turn is not whole."""
+    check_norm(rows, D, G, dtype, rows + D, z=True)
+    check_norm(rows, D, G, dtype, rows + D + 1, centered=False, act="silu")
