@@ -391,3 +391,50 @@ def test_norm_workgroups_walk_several_rows(rows, D, G, dtype):
     width: parameters' gradients add up over the turns, and the last turn is not whole."""
     check_norm(rows, D, G, dtype, rows + D, z=True)
     check_norm(rows, D, G, dtype, rows + D + 1, centered=False, act="silu")
+
+
+# ---------------------------------------------------------------------------
+# single tokens under a captured graph
+# ---------------------------------------------------------------------------
+
+@gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_steps_replay_under_a_graph(dtype):
+    """Convolution step, scan step and norm of one token captured once, states updated in
+    place, replayed token by token with eager work between: each replay equals the eager step."""
+    say("token steps under a captured graph", dtype)
+    B, D, K, N, T = 3, 72, 4, 16, 6
+    c = conv_inputs(B, T, D, K, dtype, 31)
+    s = scan_inputs(B, T, D, 1, N, dtype, 32)
+    x, z, delta = (dev(t, dtype) for t in (c["x"], s["z"], s["delta"]))
+    Bm, Cm = dev(s["Bm"], dtype), dev(s["Cm"], dtype)
+    w, b, A, skip, bias = (dev(t, F32) for t in (c["w"], c["bias"], s["A"], s["skip"], s["delta_bias"]))
+    token = [t[:, 0].clone() for t in (x, z, delta, Bm, Cm)]
+
+    def step(taps, h):
+        v, _ = lrs.mi_causal_conv_step(token[0], w, b, taps, act="silu", x_out=taps)
+        y, _ = lrs.mi_selective_scan_step(v, token[2], A, token[3], token[4], h, skip, None, bias, h_out=h)
+        return lrs.mi_group_norm_fwd(y, None, None, token[1], groups=3, centered=False)
+
+    fresh = lambda: (torch.zeros(B, K - 1, D, dtype=dtype, device="cuda"), torch.zeros(B, D, N, device="cuda"))
+    held, mine = fresh(), fresh()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(*fresh())
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(*held)
+    for t in held:
+        t.zero_()  # (capturing ran nothing; the states start where the eager ones do)
+    for t in range(T):
+        for dst, src in zip(token, (x, z, delta, Bm, Cm)):
+            dst.copy_(src[:, t])
+        graph.replay()
+        torch.cuda.synchronize()
+        got = out.clone()
+        want = step(*mine)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want), t
+        assert torch.equal(held[0], mine[0]) and torch.equal(held[1], mine[1]), t
