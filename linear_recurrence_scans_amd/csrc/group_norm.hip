@@ -344,11 +344,18 @@ struct StoreNorm {
     }
 };
 
-// How a shape is cut: lanes a group (1, 4, 16, 64, 256) and vectors a lane (up to
-// 8, or 16 of one or two elements), the smallest that hold a group; 0 vectors: the
-// wide kernel.  16384 rows bf16 with a gate, forward and backward: 4096 channels in
-// 512 groups, one vector each, 233 us with one lane a group and 466 with four; a
-// group of 4095 channels 1103 us with 16 elements a lane and 1690 in the wide kernel.
+// How a shape is cut: lanes a group (1, 4, 16, 64, 256) and vectors a lane, the
+// smallest that hold a group: up to 8, and 16 of one or two elements in the backward;
+// 0 vectors: the wide kernel.  16384 rows bf16 with a gate, forward and backward: 4096
+// channels in 512 groups, one vector each, 233 us with one lane a group and 466 with four.
+// 16 elements a lane against the wide kernel, 4096 gated rows of one group, us:
+//              forward                                 backward
+//   channels   3001       4095      6002      8190      3001       4095       6002       8190
+//   bf16       49 / 37    64 / 47   155 / 71  177 / 94  120 / 215  148 / 282  208 / 448  235 / 716
+//   fp32       200 / 42   240 / 55  312 / 112 400 / 157 247 / 227  286 / 383  510 / 582  577 / 787
+// The wide forward reads a row again from the L2 and keeps more waves; the wide backward
+// adds up its gradients in memory.  8 vectors of 16 bytes: bf16 162 / 254 and 421 / 1471
+// (16384 channels), fp32 128 / 156 and 226 / 773 (8192).
 struct NormPlan {
     int team, nv;
     int64_t slices, parts, rows;
@@ -358,7 +365,7 @@ NormPlan norm_plan(int64_t R, int64_t D, int64_t G, int vec, bool bwd) {
     const int64_t dg = D / G, n = (dg + vec - 1) / vec;
     q.team = n <= 1 ? 1 : n <= 4 ? 4 : n <= 16 ? 16 : n <= 64 ? 64 : 256;
     q.nv = 1;
-    while (q.nv < (vec <= 2 ? 16 : 8) && (int64_t)q.team * q.nv < n) q.nv *= 2;
+    while (q.nv < (vec <= 2 && bwd ? 16 : 8) && (int64_t)q.team * q.nv < n) q.nv *= 2;
     if ((int64_t)q.team * q.nv < n) q.nv = 0;
     int gps = 1;
     if (q.team < 64)
@@ -412,7 +419,7 @@ mi_status launch_norm(const NormArgs &a, const NormPlan &q, unsigned grid, hipSt
         case 2: return go<T, VEC, 2, 256, BWD>(a, grid, s);
         case 4: return go<T, VEC, 4, 256, BWD>(a, grid, s);
     }
-    if constexpr (VEC <= 2)
+    if constexpr (VEC <= 2 && BWD)
         if (q.nv == 16) return go<T, VEC, 16, 256, BWD>(a, grid, s);
     return go<T, VEC, 8, 256, BWD>(a, grid, s);
 }
