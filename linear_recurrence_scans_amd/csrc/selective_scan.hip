@@ -445,30 +445,40 @@ mi_status launch_tile(ScanArgs a, int64_t n_seg, hipStream_t s) {
     return launch_status();
 }
 
-// How a call is cut, by the number of workgroups that its channel tiles make.
+// How a call is cut, by the number of workgroups that its channel tiles make.  Times in
+// us, bf16 with z, n wide tiles (two channels a lane, one for N > 16):
 //  - 640 or more wide tiles: workgroups of 4 waves at 3 waves a SIMD, which
-//    overlap each other's folds; B = 8, T = 4096, D = 4096, N = 16, bf16 (1024):
-//    744 us, against 892 with 8 waves.  At B = 5, T = 2048 (640) wide tiles of 8
-//    waves and narrow ones take the same, 335 and 339 us.
+//    overlap each other's folds;
 //  - fewer: narrow tiles (one channel a lane) of 16 waves, while those make at
-//    least 192 workgroups: twice the workgroups, four times the waves; B = 3, T =
-//    4096, D = 4096 with z (384 wide): 300 us against 445 with wide tiles of 8
-//    waves, B = 4, T = 4096, D = 2048 (256 wide): 196 against 226.  (N > 32, whose
+//    least 192 workgroups: twice the workgroups, four times the waves.  (N > 32, whose
 //    tiles are narrow already and whose LDS holds 8 waves: 8 waves.)
-//  - fewer still: segments of the sequence, as many as make 768 workgroups of 4
-//    waves; B = 1, T = 4096, D = 2048 (64 wide): 102 us, against 121 narrow.
+//        N                     4          8          16         32         64
+//        wide / narrow
+//        n = 256, T = 2048     102 / 65   132 / 83   178 / 110  153 / 104  305 / 210
+//        n = 512, T = 2048     115 / 125  159 / 156  224 / 205  202 / 196  405 / 410
+//        n = 640, T = 2048     141 / 177  193 / 209  289 / 262  260 / 289  642 / 611
+//        n = 1024, T = 1024    108 / 137  125 / 168  203 / 222  182 / 205  399 / 421
+//  - fewer still: segments of the sequence, as many as the CUs hold at once (3
+//    workgroups of 4 waves, 2 for N > 32): more would run in a second turn.  B = 1,
+//    T = 4096, N = 16: n = 60 100 us in 12 segments and 111 in 13, n = 90 137 in 8 and 156
+//    in 9.  For N > 32 one turn up to 64 tiles and two beyond, where one leaves more CUs
+//    idle: n = 40 145 and 171, n = 64 196 and 214, n = 100 297 and 290, n = 150 472 and 411.
+//    Against narrow tiles, n = 64: N = 4 53 and 64, N = 16 103 and 101, N = 32 98 and 187,
+//    N = 64 196 and 403.
 enum FwdCut { FWD_MANY, FWD_NARROW, FWD_SEGMENTS };
 struct FwdPlan {
     FwdCut cut;
     int64_t n_seg;
 };
+constexpr int fwd_wps(int S) { return S == 16 ? 2 : 3; }  // waves a SIMD of wide tiles
+inline int64_t fwd_slots(int S, int64_t n) { return (S == 16 && n > 64 ? 2 : 1) * 256 * fwd_wps(S); }
 template <int S>
 FwdPlan fwd_plan(int64_t B, int64_t G, int64_t per, int64_t T) {
     constexpr int C = FwdTile<S>::C, L = FwdTile<S>::L;
     const int64_t n = B * G * ((per + 16 * C - 1) / (16 * C)), narrow = B * G * ((per + 15) / 16);
     if (n >= 640) return {FWD_MANY, 1};
     if (narrow >= 192) return {FWD_NARROW, 1};
-    const int64_t blocks = (T + 4 * L - 1) / (4 * L), want = (768 + n - 1) / n;
+    const int64_t blocks = (T + 4 * L - 1) / (4 * L), want = fwd_slots(S, n) / n;
     const int64_t seg = (blocks + want - 1) / want;  // blocks a segment
     // (a second launch costs the host about two blocks' time, its segments two more)
     return {FWD_SEGMENTS, blocks < 8 ? 1 : (blocks + seg - 1) / seg};
@@ -486,7 +496,7 @@ int64_t fwd_segments(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N) {
 template <typename T, int S>
 mi_status launch_fwd(const ScanArgs &a, hipStream_t s) {
     constexpr int C = FwdTile<S>::C, L = FwdTile<S>::L;
-    constexpr int WPS = S == 16 ? 2 : 3;
+    constexpr int WPS = fwd_wps(S);
     constexpr int LN = S >= 8 ? 4 : S >= 2 ? 8 : 16;  // narrow: at most 32 gates a lane, 128 registers
     const FwdPlan q = fwd_plan<S>(a.B, a.G, a.per, a.T);
     if (q.cut == FWD_NARROW) return launch_tile<T, S, 1, LN, S == 16 ? 8 : 16, S == 16 ? 2 : 4, false>(a, 1, s);

@@ -685,12 +685,14 @@ int64_t bwd_tiles(int64_t per, int64_t N) {
     return (per + w - 1) / w;
 }
 
-// Segments of the backward: none where the channel tiles make 192 workgroups (its
-// LDS holds one a CU), else as many as make 256.
+// Segments of the backward: as many as make at most 256 workgroups, since the LDS holds
+// one a CU: more would run in a second turn.  B = 1, T = 4096, N = 16, bf16: 40 tiles 133
+// us in 6 segments and 205 in 7, 90 tiles 335 in 2 and 408 in 3; 160 tiles 507 uncut and
+// 588 in 2; N = 4 and 64 alike (90 tiles: 189 and 232, 807 and 957).
 int64_t bwd_segments(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N) {
     const int64_t n = B * G * bwd_tiles(D / G, N), blk = scan_block(N), blocks = (T + blk - 1) / blk;
-    if (n >= 192 || blocks < 3) return 1;  // (a launch costs the host about half a block's time)
-    const int64_t want = (256 + n - 1) / n, seg = (blocks + want - 1) / want;
+    if (n > 128 || blocks < 3) return 1;  // (a launch costs the host about half a block's time)
+    const int64_t want = 256 / n, seg = (blocks + want - 1) / want;
     return (blocks + seg - 1) / seg;
 }
 
