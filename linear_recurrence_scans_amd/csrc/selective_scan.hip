@@ -461,10 +461,11 @@ mi_status launch_tile(ScanArgs a, int64_t n_seg, hipStream_t s) {
 //  - fewer still: segments of the sequence, as many as the CUs hold at once (3
 //    workgroups of 4 waves, 2 for N > 32): more would run in a second turn.  B = 1,
 //    T = 4096, N = 16: n = 60 100 us in 12 segments and 111 in 13, n = 90 137 in 8 and 156
-//    in 9.  For N > 32 one turn up to 64 tiles and two beyond, where one leaves more CUs
-//    idle: n = 40 145 and 171, n = 64 196 and 214, n = 100 297 and 290, n = 150 472 and 411.
-//    Against narrow tiles, n = 64: N = 4 53 and 64, N = 16 103 and 101, N = 32 98 and 187,
-//    N = 64 196 and 403.
+//    in 9.  Against narrow tiles, n = 64: N = 4 53 and 64, N = 16 103 and 101, N = 32 98 and
+//    187, N = 64 192 and 403 us.  At most 4 sqrt(blocks) of them, a block being 4 waves'
+//    steps: each folds all that come before it.  B = 1, T = 8192, N = 16, 256 blocks: D =
+//    64 101 us in 256 segments, 47 in 128, 41 in 64 and 52 in 32; N = 64, 512 blocks, D =
+//    64 454 in 256, 138 in 128, 72 in 64; T = 65536, D = 16 183 in 683, 100 in 128.
 enum FwdCut { FWD_MANY, FWD_NARROW, FWD_SEGMENTS };
 struct FwdPlan {
     FwdCut cut;
@@ -478,7 +479,9 @@ FwdPlan fwd_plan(int64_t B, int64_t G, int64_t per, int64_t T) {
     const int64_t n = B * G * ((per + 16 * C - 1) / (16 * C)), narrow = B * G * ((per + 15) / 16);
     if (n >= 640) return {FWD_MANY, 1};
     if (narrow >= 192) return {FWD_NARROW, 1};
-    const int64_t blocks = (T + 4 * L - 1) / (4 * L), want = fwd_slots(S, n) / n;
+    const int64_t blocks = (T + 4 * L - 1) / (4 * L), fill = fwd_slots(S, n) / n;
+    const int64_t deep = (int64_t)(4.0 * sqrt((double)blocks));
+    const int64_t want = fill < deep ? fill : deep < 1 ? 1 : deep;
     const int64_t seg = (blocks + want - 1) / want;  // blocks a segment
     // (a second launch costs the host about two blocks' time, its segments two more)
     return {FWD_SEGMENTS, blocks < 8 ? 1 : (blocks + seg - 1) / seg};
