@@ -6,11 +6,16 @@
 // steps before them are read again (they are in the caches: the neighbouring
 // wave reads them too).  All of a wave's rows are loaded before the first is
 // used, so a wave keeps R + K - 1 rows in flight.  Measured (MI355X, K = 4, SiLU,
-// bf16): B = 8, T = 8192, D = 4096 204 us, 5.3 TB/s of x and y, a little above a
-// large copy's 4.9; with 16 bytes a lane (140 registers for 74) 211 us, with 8, 24
+// bf16): B = 8, T = 8192, D = 4096 202 us, 5.3 TB/s of x and y (a streaming read and
+// write of that size 5.7); with 16 bytes a lane (140 registers for 74) 211 us, with 8, 24
 // and 32 steps a wave 218, 206 and 214 us.  Forward and backward at B = 4, T = 4096,
-// D = 2048 together 72 to 79 us; with 16 bytes and 8 steps a batch in the backward
-// (115 registers for 98) 87 us.
+// D = 2048 together 75 us on the GPU; with 16 bytes and 8 steps a batch in the backward
+// (115 registers for 98) 87 us.  fp32: B = 4, T = 8192, D = 4096 195 us (5.5 TB/s); forward
+// and backward as above 123 us.
+//
+// Sums over steps (dw, dbias) are fp32: a wave's 16 to 64 steps, four waves, then the
+// partial rows.  Their error, 1.2e-7 of the gradient's norm at B = 5, T = 1037, is twice
+// what sums in 64 bits leave after one rounding; y and dx are off by 0.7e-7.
 #include "block_ops.hpp"
 #include "checks.hpp"
 
@@ -306,7 +311,10 @@ mi_status with_type(mi_dtype dt, int64_t K, F f) {
 
 // Steps a wave of the backward walks.  Every wave repeats K - 1 steps, so long
 // runs waste less; short runs give more waves.  The longest run of 16, 32, 64
-// that still makes 4096 waves (16 a CU).
+// that still makes 4096 waves (16 a CU).  K = 4, bf16, us with 16 / 32 / 64 steps (waves
+// at 64): B = 8, T = 8192, D = 4096 (16384) 399 / 353 / 344; B = 4, T = 4096, D = 2048
+// (2048) 56 / 48 / 56; B = 2, T = 2048, D = 1024 (256) 20 / 28 / 46; few channels, B = 8,
+// T = 8192, D = 64 (1024), where 32 would be better: 47 / 41 / 52.
 int bwd_rows(int64_t B, int64_t T, int64_t D, int64_t esize) {
     const int64_t tile = 64 * (8 / esize);
     int r = 64;

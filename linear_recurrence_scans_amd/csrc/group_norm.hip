@@ -6,8 +6,10 @@
 // sums (the variance about the mean, no cancellation).  A lane keeps its
 // channels' parameters, and in the backward their gradients' sums, in registers
 // over all the rows its workgroup walks.  The bound is HBM: forward 2 to 3,
-// backward 3 to 5 tensors moved once.  Measured (MI355X, 16384 x 4096 bf16, 32
-// groups, gated): forward 75 us (5.4 TB/s), backward 138 (4.9 TB/s) and its sums 7.
+// backward 3 to 5 tensors moved once.  Measured (MI355X, 16384 x 4096, gated): bf16 in
+// 32 groups forward 75 us (5.4 TB/s), backward 142 (4.7 TB/s) and its sums 6; bf16 in one
+// group forward 69 (5.9 TB/s), both 240; fp32 in 32 groups 176 (4.6 TB/s) and 459, in one
+// group 153 (5.3 TB/s) and 466.
 #include "block_ops.hpp"
 #include "checks.hpp"
 
@@ -371,7 +373,11 @@ NormPlan norm_plan(int64_t R, int64_t D, int64_t G, int vec, bool bwd) {
     if (q.team < 64)
         while (gps < 64 / q.team && gps < G) gps *= 2;
     q.slices = q.team == 256 ? G : (G + gps - 1) / gps;
-    // about 2048 workgroups (8 a CU); the backward at most 512 partial rows
+    // about 2048 workgroups (8 a CU); the backward at most 512 partial rows, which the
+    // closing sum reads.  16384 rows bf16, gated, us with 1024 / 2048 / 4096 workgroups
+    // forward: 4096 channels in 32 groups 72 / 74 / 65, in one 71 / 71 / 71, 1024 in one 36 /
+    // 31 / 29; with 256 / 512 / 1024 rows backward (and the sum): 4096 in 32 groups all 156,
+    // in one 298 / 182 / 207, 1024 in one 140 / 86 / 72, 64 in one 20 / 22 / 32
     const int64_t unit = q.team == 256 ? 1 : 4 * (64 / q.team / gps);  // rows of one turn
     const int64_t turns = (R + unit - 1) / unit;
     int64_t parts = (2048 + q.slices - 1) / q.slices;

@@ -9,8 +9,8 @@
 // the 6 to 8 bytes a channel-step moves: the vector ALU is the bound.  All in all a
 // state-step takes 12 slots of 4 cycles (softplus, the gate silu(z), conversions and
 // joins the rest).  Measured (MI355X, N = 16, bf16): B = 8, T = 4096, D = 4096 740 us,
-// the vector ALU busy for 82 to 89 % of it; B = 1, T = 8192, D = 4096 with z 213 us,
-// 84 %.  The step of 64 sequences, D = 4096: 8.6 us, 4.2 TB/s.
+// the vector ALU busy for 82 % of it; B = 1, T = 8192, D = 4096 with z 191 us, 84 %.
+// The step of 64 sequences, D = 4096: 8.3 us, 4.3 TB/s.
 #include "checks.hpp"
 #include "selective_scan.hpp"
 

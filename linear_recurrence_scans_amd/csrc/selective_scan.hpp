@@ -157,10 +157,9 @@ __device__ __forceinline__ typename Pack<T, N>::raw_t buf_read(rsrc_t r, uint32_
 // is therefore held as its square root, at most 2^127, and applied twice, which
 // covers whatever a normal state and its result can span.  (A NaN in P is one in
 // the run's scan from zero too.)  The forward's blocks use P itself and redo a fold
-// that ends in no finite value step by step: 744 us for B = 8, T = 4096, D = 4096,
-// N = 16, bf16, against 760 with roots and 739 with neither; the backward has no
-// registers for that (774 us for B = 4, T = 4096, D = 2048 with its forward, against
-// 730 with roots and 724).
+// that ends in no finite value step by step: for B = 8, T = 4096, D = 4096, N = 16, bf16
+// that costs 2 to 5 us of 740, roots 21; the backward has no registers for it (50 us of
+// 726 for B = 4, T = 4096, D = 2048 with its forward, roots 6).
 __device__ __forceinline__ float root_product(float e) {  // e: log2 of the product
     return __builtin_amdgcn_exp2f(fminf(0.5f * e, 127.f));
 }

@@ -7,10 +7,11 @@
 // (keeping a_t h_{t-1}) and in reverse from its true g.  Per state-step: gate 3
 // issue slots (mul, exp2), local scans 4, states 2 to 4, gradients 7.
 //
-// Measured (MI355X, N = 16, bf16, z): B = 4, T = 4096, D = 2048 540 us (256
-// workgroups, one a CU), 26 slots a state-step, the vector ALU busy for 72 % of it;
-// the rest are the two meetings a block, and LDS latency that two waves a SIMD do
-// not hide.
+// Measured (MI355X, N = 16, bf16, z): B = 4, T = 4096, D = 2048 493 us (256
+// workgroups, one a CU) and 23 for the closing sums, 26 slots a state-step, the vector ALU
+// busy for 73 % of it; the rest are the two meetings a block, and LDS latency that two
+// waves a SIMD do not hide.  Forward and backward of that size in us, and the MB of partial
+// sums: N = 4 460 (34), 8 555 (67), 16 731 (135), 32 1747 (538), 64 3402 (1076).
 //
 // dBm and dCm sum over the channels of a group: C of them in the lane, sixteen
 // lanes through LDS, the tiles of a group through partial rows that
